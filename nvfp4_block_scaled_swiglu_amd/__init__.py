@@ -16,6 +16,7 @@ Functions carry the C names:
 * ``nvfp4_gemm_bf16out(a, w)``        - block-scaled GEMM, FP32 accumulation, BF16 out
 * ``nvfp4_silu_bf16(x)``              - the producer's bf16 silu, elementwise (self-test)
 * size helpers ``nvfp4_padded_rows``, ``nvfp4_qdata_bytes``, ``nvfp4_scale_bytes``, ...
+* the MXFP4 operators (``mxfp4_*``: quantization, product, paged cache, attention) of ``mxfp4.py``
 """
 from __future__ import annotations
 
@@ -92,7 +93,8 @@ def lib() -> ctypes.CDLL:
                 raise ImportError(f"{LIB_PATH} is missing: build it with "
                                   "`python nvfp4_block_scaled_swiglu_amd/build.py`")
             l = ctypes.CDLL(LIB_PATH)
-            for name, (res, args) in SIGNATURES.items():
+            from .mxfp4 import SIGNATURES as mx_signatures
+            for name, (res, args) in {**SIGNATURES, **mx_signatures}.items():
                 fn = getattr(l, name)
                 fn.restype = res
                 fn.argtypes = args
@@ -490,3 +492,9 @@ def nvfp4_silu_bf16(x, out=None, stream=None):
     out = torch.empty_like(x) if out is None else out
     _call("nvfp4_silu_bf16", x.data_ptr(), out.data_ptr(), x.numel(), _stream_handle(stream))
     return out
+
+
+from .mxfp4 import (  # noqa: E402  (the operators use the names above)
+    Mxfp4Cache, Mxfp4Tensor, empty_mxfp4, empty_mxfp4_cache, mxfp4_attention, mxfp4_attention_workspace_bytes,
+    mxfp4_cache_append, mxfp4_cache_read, mxfp4_dequantize, mxfp4_gemm_bf16out, mxfp4_qdata_bytes, mxfp4_quantize,
+    mxfp4_quantize_swiglu, mxfp4_scale_bytes, mxfp4_scale_cols)

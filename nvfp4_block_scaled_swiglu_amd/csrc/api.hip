@@ -13,6 +13,7 @@
 #include <mutex>
 
 #include "nvfp4.h"
+#include "api.hpp"
 #include "common.hpp"
 
 namespace nvfp4 {
@@ -38,6 +39,7 @@ hipError_t launch_mfma_ceiling(uint64_t* out, int64_t workgroups, int64_t iters,
 hipError_t launch_hbm_stream(const void* src, int64_t read_bytes, void* dst, int64_t write_bytes, int workgroups,
                              hipStream_t stream);
 int64_t hbm_stream_chunk_bytes();
+hipError_t mx_gemm_setup();
 }  // namespace nvfp4
 
 namespace {
@@ -149,6 +151,8 @@ int ensure_device(DeviceState** out) {
                             (int)nvfp4::gemm_smem_bytes(kind));
     if (e != hipSuccess) return fail(NVFP4_ERR_LAUNCH, "gemm LDS attribute: %s", hipGetErrorString(e));
   }
+  e = nvfp4::mx_gemm_setup();
+  if (e != hipSuccess) return fail(NVFP4_ERR_LAUNCH, "mx gemm LDS attribute: %s", hipGetErrorString(e));
 
   e = nvfp4::silu_table_address(&st.silu_table);
   if (e != hipSuccess) return fail(NVFP4_ERR_LAUNCH, "silu table address: %s", hipGetErrorString(e));
@@ -213,6 +217,27 @@ int check_quant_args(const void* x, int64_t ldx, const void* u, int64_t ldu, boo
 }
 
 }  // namespace
+
+namespace nvfp4 {
+
+int api_fail(int status, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(t_last_error, sizeof(t_last_error), fmt, ap);
+  va_end(ap);
+  return status;
+}
+
+int api_ok() { return ok(); }
+
+int api_device(const uint16_t** silu_table) {
+  DeviceState* st = nullptr;
+  const int rc = ensure_device(&st);
+  if (rc == NVFP4_OK) *silu_table = st->silu_table;
+  return rc;
+}
+
+}  // namespace nvfp4
 
 extern "C" {
 

@@ -1,0 +1,391 @@
+// mx_gemm.hip - MXFP4 product with FP32 accumulation and BF16 output (gfx950).
+//
+//   D[m, n] = RN_bf16(sum_k A[m, k] W[n, k]),  A, W = e2m1 * 2^(S - 127)
+//
+// The scaled matrix instructions take E2M1 codes and E8M0 scales as they are stored, so
+// nothing is converted: 32x32x64 multiplies 32 rows by 32 columns over two blocks of 32,
+// each lane giving the 16 code bytes and one scale byte of its (row, block). Every product
+// is exact and the sums are fp32. The rate is four times that of fp16, so a K step has a
+// quarter of the time to bring its operands that the fp16 form has per element.
+#include "mx.hpp"
+
+namespace nvfp4 {
+
+namespace {
+
+typedef __attribute__((ext_vector_type(8))) int i32x8_t;
+typedef __attribute__((ext_vector_type(4))) float f32x4_t;
+typedef __attribute__((address_space(3))) void lds_ptr_t;
+
+struct MxGemmArgs {
+  const uint8_t* aq;
+  const uint8_t* as;
+  const uint8_t* wq;
+  const uint8_t* ws;
+  uint16_t* d;
+  int64_t ldd, m, n, k;
+  int groups;            // scale columns / 4 = K steps of 128
+  int tiles_m, tiles_n;
+  bool wide;             // D rows take 16-byte stores
+};
+
+__device__ __forceinline__ i32x8_t fp4_operand(const u32x4_t& c) {
+  return i32x8_t{(int)c[0], (int)c[1], (int)c[2], (int)c[3], 0, 0, 0, 0};
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  bf16x2_t c;
+  c[0] = (__bf16)lo;
+  c[1] = (__bf16)hi;
+  return as_u32(c);
+}
+
+// ---- tiles ---------------------------------------------------------------------------------
+// A workgroup of 4 waves (2 x 2) computes (64 FM) x (64 FN); a wave owns FM x FN tiles of
+// 32 x 32. K advances 128 per step: 64 code bytes a row and one 512-byte scale tile per
+// 128 rows. Direct-to-LDS loads bring step ks + kStages while step ks is multiplied.
+// A step has two halves of one MFMA per tile each: while the MFMAs of a half run, the
+// fragments of the next are read from LDS. The barrier sits between the halves: every wave
+// has then read both halves of step ks, whose stage takes the next loads, and each has
+// seen its own loads of step ks + 1 land.
+constexpr int kWaves = 4;
+constexpr int kStages = 3;
+constexpr int kBand = 8;  // M tiles per traversal band
+
+template <int FM, int FN>
+struct Shape {
+  static constexpr int TM = 64 * FM, TN = 64 * FN;
+  static constexpr int CodesA = TM * 64, CodesW = TN * 64;
+  static constexpr int ScaleA = TM / 128 * 512, ScaleW = TN / 128 * 512;
+  static constexpr int Stage = CodesA + CodesW + ScaleA + ScaleW;
+  static constexpr int LoadsA = CodesA / 1024 / kWaves, LoadsW = CodesW / 1024 / kWaves;
+  static constexpr int LoadsS = (ScaleA + ScaleW) / 256 / kWaves;  // a dword a lane
+  static constexpr int Loads = LoadsA + LoadsW + LoadsS;
+  static constexpr int RowBytes = 32 * FN * 2 + 16;                 // epilogue staging, padded
+  static constexpr int Staging = kWaves * 32 * RowBytes;
+  static constexpr int Lds = kStages * Stage > Staging ? kStages * Stage : Staging;
+  static_assert(CodesA % (1024 * kWaves) == 0 && CodesW % (1024 * kWaves) == 0, "even code loads");
+  static_assert((ScaleA + ScaleW) % (256 * kWaves) == 0, "even scale loads");
+  static_assert((kStages - 2) * Loads < 64, "vmcnt immediate");
+};
+
+// where 16-byte chunk c of row r lies in the row's 64 LDS bytes: fragment reads (32 rows,
+// one chunk) then meet every bank
+__device__ __forceinline__ int chunk_at(int r, int c) { return c ^ (((r >> 1) ^ (r >> 2)) & 3); }
+
+__device__ __forceinline__ void barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// s_waitcnt vmcnt(n) lgkmcnt(15) expcnt(7)
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));
+}
+
+template <int FM, int FN>
+__global__ __launch_bounds__(64 * kWaves, 1) void mx_gemm_kernel(MxGemmArgs a) {
+  using T = Shape<FM, FN>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int lr = lane & 31, h = lane >> 5;
+
+  // Workgroups go round-robin to the 8 XCDs: each XCD gets one contiguous range of tiles,
+  // numbered in bands of kBand M tiles, so that its L2 keeps the band's rows of A.
+  const int total = a.tiles_m * a.tiles_n;
+  const int per = total / 8, rem = total % 8, x = blockIdx.x & 7;
+  const int tile = x * per + (x < rem ? x : rem) + (blockIdx.x >> 3);
+  const int band = tile / (kBand * a.tiles_n);
+  const int inside = tile - band * kBand * a.tiles_n;
+  const int height = a.tiles_m - band * kBand < kBand ? a.tiles_m - band * kBand : kBand;
+  const int64_t m0 = (int64_t)(band * kBand + inside % height) * T::TM;
+  const int64_t n0 = (int64_t)(inside / height) * T::TN;
+
+  // Buffers of the tile's own rows: reads past them return zero (codes 0 under scale 0).
+  const int krow = (int)(a.k >> 1);
+  const int rows_a = (int)(a.m - m0 < T::TM ? a.m - m0 : T::TM), rows_w = (int)(a.n - n0 < T::TN ? a.n - n0 : T::TN);
+  const int srow = a.groups * 512;
+  __amdgpu_buffer_rsrc_t rA =
+      __builtin_amdgcn_make_buffer_rsrc((void*)(a.aq + m0 * krow), 0, rows_a * krow, 0x00020000);
+  __amdgpu_buffer_rsrc_t rW =
+      __builtin_amdgcn_make_buffer_rsrc((void*)(a.wq + n0 * krow), 0, rows_w * krow, 0x00020000);
+  __amdgpu_buffer_rsrc_t rSA = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)(a.as + (m0 >> 7) * srow), 0, ((rows_a + 127) >> 7) * srow, 0x00020000);
+  __amdgpu_buffer_rsrc_t rSW = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)(a.ws + (n0 >> 7) * srow), 0, ((rows_w + 127) >> 7) * srow, 0x00020000);
+
+  // Load idx of this wave's share of step ks. Code load j covers rows 16 j .. 16 j + 15;
+  // lane L writes LDS bytes 16 L .. of that KiB, which hold chunk chunk_at(row, L & 3) (an
+  // involution) of row 16 j + L / 4. Chunks past K (and whole steps past the last) read
+  // past the buffer, where there is nothing but zeros.
+  auto issue = [&](int ks, int stage, int idx) __attribute__((always_inline)) {
+    uint8_t* st = smem + stage * T::Stage;
+    if (idx < T::LoadsA + T::LoadsW) {
+      const bool is_a = idx < T::LoadsA;
+      const int j = wave + (is_a ? idx : idx - T::LoadsA) * kWaves;
+      const int row = j * 16 + (lane >> 2);
+      const int c = chunk_at(row, lane & 3);
+      const int kb = ks * 64 + c * 16;
+      const int off = kb < krow ? row * krow + kb : 0x7FFFFFF0;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(is_a ? rA : rW, (lds_ptr_t*)(st + (is_a ? 0 : T::CodesA) + j * 1024), 16,
+                                               off, 0, 0, 0);
+    } else {
+      const int q = wave * T::LoadsS + (idx - T::LoadsA - T::LoadsW);  // 256-byte piece of the scales
+      const bool is_a = q * 256 < T::ScaleA;
+      const int rel = is_a ? q : q - T::ScaleA / 256;
+      const int off = (rel >> 1) * srow + ks * 512 + (rel & 1) * 256 + lane * 4;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(is_a ? rSA : rSW, (lds_ptr_t*)(st + T::CodesA + T::CodesW + q * 256), 4,
+                                               off, 0, 0, 0);
+    }
+  };
+  // half kk: lane half h takes block (chunk) 2 kk + h of the step
+  auto read_codes = [&](int stage, int kk, u32x4_t (&ca)[FM], u32x4_t (&cw)[FN]) __attribute__((always_inline)) {
+    const uint8_t* st = smem + stage * T::Stage;
+    const int c = 2 * kk + h;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int r = (wm * FM + i) * 32 + lr;
+      ca[i] = *(const u32x4_t*)(st + r * 64 + chunk_at(r, c) * 16);
+    }
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const int r = (wn * FN + j) * 32 + lr;
+      cw[j] = *(const u32x4_t*)(st + T::CodesA + r * 64 + chunk_at(r, c) * 16);
+    }
+  };
+  // the four scale bytes of each row, moved so that bytes 0 and 2 are the lane half's
+  auto read_scales = [&](int stage, uint32_t (&sa)[FM], uint32_t (&sw)[FN]) __attribute__((always_inline)) {
+    const uint8_t* ss = smem + stage * T::Stage + T::CodesA + T::CodesW;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int f = wm * FM + i;  // 32-row group of the tile
+      sa[i] = *(const uint32_t*)(ss + (f >> 2) * 512 + lr * 16 + (f & 3) * 4);
+    }
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const int f = wn * FN + j;
+      sw[j] = *(const uint32_t*)(ss + T::ScaleA + (f >> 2) * 512 + lr * 16 + (f & 3) * 4);
+    }
+  };
+
+  f32x16_t acc[FN][FM];
+#pragma unroll
+  for (int j = 0; j < FN; ++j)
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[j][i][r] = 0.0f;
+
+#pragma unroll
+  for (int s = 0; s < kStages; ++s)
+#pragma unroll
+    for (int idx = 0; idx < T::Loads; ++idx) issue(s, s, idx);
+  wait_loads<(kStages - 1) * T::Loads>();
+  barrier();
+
+  u32x4_t ca[2][FM], cw[2][FN];
+  uint32_t sa[2][FM], sw[2][FN];
+  read_scales(0, sa[0], sw[0]);
+  read_codes(0, 0, ca[0], cw[0]);
+
+  auto kstep = [&](int ks, int stage, int set) __attribute__((always_inline)) {
+    const int next = stage + 1 == kStages ? 0 : stage + 1;
+    read_codes(stage, 1, ca[1], cw[1]);
+    uint32_t ha[FM], hw[FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) ha[i] = sa[set][i] >> (8 * h);
+#pragma unroll
+    for (int j = 0; j < FN; ++j) hw[j] = sw[set][j] >> (8 * h);
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+        acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fp4_operand(cw[0][j]), fp4_operand(ca[0][i]),
+                                                                    acc[j][i], 4, 4, 0, (int)hw[j], 0, (int)ha[i]);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this stage's reads are done
+    wait_loads<(kStages - 2) * T::Loads>();
+    barrier();
+#pragma unroll
+    for (int idx = 0; idx < T::Loads; ++idx) issue(ks + kStages, stage, idx);
+    read_scales(next, sa[set ^ 1], sw[set ^ 1]);
+    read_codes(next, 0, ca[0], cw[0]);
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+        acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fp4_operand(cw[1][j]), fp4_operand(ca[1][i]),
+                                                                    acc[j][i], 4, 4, 2, (int)hw[j], 2, (int)ha[i]);
+  };
+  int stage = 0, ks = 0;
+  for (; ks + 1 < a.groups; ks += 2) {
+    kstep(ks, stage, 0);
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+    kstep(ks + 1, stage, 1);
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+  }
+  if (ks < a.groups) kstep(ks, stage, 0);
+
+  // ---- epilogue: 32 rows at a time through the wave's part of LDS, so that a store writes
+  // whole row pieces. The loads past the last step are still writing zeros: wait first. ----
+  wait_loads<0>();
+  barrier();
+  uint8_t* stg = smem + wave * (32 * T::RowBytes);
+  constexpr int kChunks = 32 * FN / 8, kRowsPerStore = 64 / kChunks;
+  const int64_t row0 = m0 + wm * FM * 32, col0 = n0 + wn * FN * 32;
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *(u32x2_t*)(stg + lr * T::RowBytes + (j * 32 + q * 8 + h * 4) * 2) =
+            u32x2_t{pack_bf16(acc[j][i][q * 4], acc[j][i][q * 4 + 1]), pack_bf16(acc[j][i][q * 4 + 2], acc[j][i][q * 4 + 3])};
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int it = 0; it < 32 / kRowsPerStore; ++it) {
+      const int r = it * kRowsPerStore + lane / kChunks, ch = lane % kChunks;
+      const u32x4_t v = *(const u32x4_t*)(stg + r * T::RowBytes + ch * 16);
+      const int64_t m = row0 + i * 32 + r, n = col0 + ch * 8;
+      if (m < a.m && n < a.n) {
+        uint16_t* dst = a.d + m * a.ldd + n;
+        if (a.wide) {
+          *(u32x4_t*)dst = v;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (n + e < a.n) dst[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+        }
+      }
+    }
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    asm volatile("" ::: "memory");
+  }
+}
+
+// ---- few rows ------------------------------------------------------------------------------
+// Up to 64 rows of A: the weight is read once and that is all there is to it. A workgroup
+// takes 16 NT columns and its waves split K, so that n / (16 NT) workgroups of 8 waves keep
+// enough loads in flight; operands go from memory to registers (16x16x128: lane (r, u) has
+// row r, block u of the step). The waves' sums are joined in LDS in wave order.
+constexpr int kThinWaves = 8;
+constexpr int kThinSteps = 4;  // K steps of 128 in flight per wave
+
+template <int MT, int NT>
+__global__ __launch_bounds__(64 * kThinWaves, 2) void mx_gemm_thin_kernel(MxGemmArgs a) {
+  __shared__ float red[kThinWaves * MT * NT * 256];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, u = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * NT);
+  const int krow = (int)(a.k >> 1), srow = a.groups * 512;
+  const int rows_w = (int)(a.n - n0 < 16 * NT ? a.n - n0 : 16 * NT);
+  __amdgpu_buffer_rsrc_t rA = __builtin_amdgcn_make_buffer_rsrc((void*)a.aq, 0, (int)a.m * krow, 0x00020000);
+  __amdgpu_buffer_rsrc_t rW = __builtin_amdgcn_make_buffer_rsrc((void*)(a.wq + n0 * krow), 0, rows_w * krow, 0x00020000);
+  __amdgpu_buffer_rsrc_t rSA = __builtin_amdgcn_make_buffer_rsrc((void*)a.as, 0, srow, 0x00020000);
+  __amdgpu_buffer_rsrc_t rSW =
+      __builtin_amdgcn_make_buffer_rsrc((void*)(a.ws + (n0 >> 7) * srow), 0, srow, 0x00020000);
+  const int nrow = (int)(n0 & 127);  // the columns' rows in their 128-row scale tile
+  auto scale_at = [&](int row) __attribute__((always_inline)) { return (row & 31) * 16 + (row >> 5) * 4; };
+
+  f32x4_t acc[NT][MT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[j][i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+
+  for (int k0 = wave * kThinSteps; k0 < a.groups; k0 += kThinWaves * kThinSteps) {
+    u32x4_t cw[kThinSteps][NT], ca[kThinSteps][MT];
+    uint32_t sw[kThinSteps][NT], sa[kThinSteps][MT];
+#pragma unroll
+    for (int s = 0; s < kThinSteps; ++s) {
+      const int kb = (k0 + s) * 64 + u * 16;
+      const bool in = kb < krow;  // past K: codes 0
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int row = j * 16 + r;
+        cw[s][j] = __builtin_amdgcn_raw_buffer_load_b128(rW, in ? row * krow + kb : 0x7FFFFFF0, 0, 0);
+        sw[s][j] = __builtin_amdgcn_raw_buffer_load_b32(rSW, in ? (k0 + s) * 512 + scale_at(nrow + row) : 0x7FFFFFF0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const int row = i * 16 + r;
+        ca[s][i] = __builtin_amdgcn_raw_buffer_load_b128(rA, in ? row * krow + kb : 0x7FFFFFF0, 0, 0);
+        sa[s][i] = __builtin_amdgcn_raw_buffer_load_b32(rSA, in ? (k0 + s) * 512 + scale_at(row) : 0x7FFFFFF0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < kThinSteps; ++s)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+          acc[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              fp4_operand(cw[s][j]), fp4_operand(ca[s][i]), acc[j][i], 4, 4, 0, (int)(sw[s][j] >> (8 * u)), 0,
+              (int)(sa[s][i] >> (8 * u)));
+  }
+  // lane (r, u) holds row m = r, columns 4u .. 4u + 3 of each 16 x 16 tile
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int i = 0; i < MT; ++i) *(f32x4_t*)(red + ((wave * NT + j) * MT + i) * 256 + lane * 4) = acc[j][i];
+  __syncthreads();
+  for (int e = threadIdx.x; e < MT * NT * 256; e += 64 * kThinWaves) {
+    // e: column within the workgroup's fastest, then row, so that stores run along D's rows
+    const int col = e % (16 * NT), row = e / (16 * NT);
+    const int at = ((col >> 4) * MT + (row >> 4)) * 256 + (((col & 15) >> 2) * 16 + (row & 15)) * 4 + (col & 3);
+    float y = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kThinWaves; ++w) y += red[w * MT * NT * 256 + at];
+    if (row < a.m && n0 + col < a.n) a.d[row * a.ldd + n0 + col] = (uint16_t)pack_bf16(y, 0.0f);
+  }
+}
+
+template <int FM, int FN>
+hipError_t launch_tiles(MxGemmArgs a, hipStream_t stream) {
+  using T = Shape<FM, FN>;
+  a.tiles_m = (int)((a.m + T::TM - 1) / T::TM);
+  a.tiles_n = (int)((a.n + T::TN - 1) / T::TN);
+  mx_gemm_kernel<FM, FN><<<a.tiles_m * a.tiles_n, 64 * kWaves, T::Lds, stream>>>(a);
+  return hipGetLastError();
+}
+
+template <int MT, int NT>
+hipError_t launch_thin(const MxGemmArgs& a, hipStream_t stream) {
+  mx_gemm_thin_kernel<MT, NT><<<(unsigned)((a.n + 16 * NT - 1) / (16 * NT)), 64 * kThinWaves, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t mx_gemm_setup() {
+  hipError_t e = hipFuncSetAttribute((const void*)mx_gemm_kernel<4, 4>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                     Shape<4, 4>::Lds);
+  if (e == hipSuccess)
+    e = hipFuncSetAttribute((const void*)mx_gemm_kernel<2, 2>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                            Shape<2, 2>::Lds);
+  return e;
+}
+
+hipError_t launch_mx_gemm(const uint8_t* aq, const uint8_t* as, const uint8_t* wq, const uint8_t* ws, uint16_t* d,
+                          int64_t ldd, int64_t m, int64_t n, int64_t k, hipStream_t stream) {
+  MxGemmArgs a{aq, as, wq, ws, d, ldd, m, n, k, (int)((k / kMxBlock + 3) / 4), 0, 0,
+               n % 8 == 0 && ldd % 8 == 0 && ((uintptr_t)d & 15u) == 0};
+  if (m <= 16) return launch_thin<1, 1>(a, stream);
+  if (m <= 32) return launch_thin<2, 1>(a, stream);
+  if (m <= 64) return launch_thin<4, 1>(a, stream);
+  // whole 256 x 256 tiles need the fewest operand bytes per product; with too few of them
+  // to give every CU one, quarters
+  const int64_t big = ((m + 255) / 256) * ((n + 255) / 256);
+  if (big < 256) return launch_tiles<2, 2>(a, stream);
+  return launch_tiles<4, 4>(a, stream);
+}
+
+}  // namespace nvfp4
