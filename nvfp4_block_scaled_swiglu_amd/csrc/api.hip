@@ -40,6 +40,7 @@ hipError_t launch_hbm_stream(const void* src, int64_t read_bytes, void* dst, int
                              hipStream_t stream);
 int64_t hbm_stream_chunk_bytes();
 hipError_t mx_gemm_setup();
+hipError_t mx_attention_setup();
 }  // namespace nvfp4
 
 namespace {
@@ -152,7 +153,8 @@ int ensure_device(DeviceState** out) {
     if (e != hipSuccess) return fail(NVFP4_ERR_LAUNCH, "gemm LDS attribute: %s", hipGetErrorString(e));
   }
   e = nvfp4::mx_gemm_setup();
-  if (e != hipSuccess) return fail(NVFP4_ERR_LAUNCH, "mx gemm LDS attribute: %s", hipGetErrorString(e));
+  if (e == hipSuccess) e = nvfp4::mx_attention_setup();
+  if (e != hipSuccess) return fail(NVFP4_ERR_LAUNCH, "MXFP4 kernels' LDS attribute: %s", hipGetErrorString(e));
 
   e = nvfp4::silu_table_address(&st.silu_table);
   if (e != hipSuccess) return fail(NVFP4_ERR_LAUNCH, "silu table address: %s", hipGetErrorString(e));

@@ -177,7 +177,7 @@ int check_attention(const mxfp4_cache* cache, const mxfp4_batch* batch, int64_t 
     return api_fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "more than 65536 heads, or 2^31 rows x heads of a group");
   *plan = nvfp4::mx_attention_plan(b->tokens, b->batch, heads, c->kv_heads, c->head_dim, max_kv, window, sinks);
   if ((b->tokens * (heads / c->kv_heads) / 16 + b->batch) * c->kv_heads > kMostGroups ||
-      b->tokens * heads / 4 > kMostGroups)
+      b->tokens * heads > kMostGroups)
     return api_fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "too many rows and heads for one call");
   return NVFP4_OK;
 }

@@ -19,30 +19,32 @@ struct MxAttnArgs {
   float2* part_ml;  // [splits, tokens, heads] maximum (log2) and sum
 };
 
+constexpr int kMxMostSplits = 256;
+
 // How a call is cut, from its sizes alone.
 struct MxAttnPlan {
-  bool coop;      // a workgroup's four waves share its rows and split the tokens
-  int row_tiles;  // 16-row tiles of a wave
+  bool few;       // the form for few rows
+  int row_tiles;  // its 16-row tiles of a workgroup
   int splits;     // pieces of the token axis, joined by a second launch
 };
 
 // Rows: the packed rows (rows x heads of a group) of an average sequence. Up to 64 of them
-// fit one wave, and the four waves of a workgroup split the tokens; beyond that every wave
-// takes rows of its own.
+// (32 at head_dim 256) are one workgroup's of the few-rows form, whose four waves split the
+// tokens; beyond that the prompt form gives every wave rows of its own.
 // Splits: enough workgroups to fill 256 CUs four times where the rows alone do not, but
 // at least kMinTiles 32-token tiles a wave, so that a split is more than its own start
 // and its share of the join.
 inline MxAttnPlan mx_attention_plan(int64_t tokens, int64_t batch, int64_t heads, int64_t kv_heads, int64_t head_dim,
                                     int64_t max_kv, int64_t window, int64_t sinks) {
-  constexpr int64_t kWanted = 1024, kMinTiles = 2, kMostSplits = 256;
+  constexpr int64_t kWanted = 1024, kMinTiles = 2;
   MxAttnPlan p{true, 1, 1};
   if (tokens <= 0 || batch <= 0) return p;
   const int64_t group = heads / kv_heads;
   const int64_t rows = (tokens + batch - 1) / batch * group;
   const int most = head_dim == 256 ? 2 : 4;
-  p.coop = rows <= 16 * most;
-  p.row_tiles = p.coop ? (rows <= 16 ? 1 : rows <= 32 ? 2 : most) : most;
-  const int64_t per_group = 16 * p.row_tiles * (p.coop ? 1 : 4);
+  p.few = rows <= 16 * most;
+  p.row_tiles = rows <= 16 ? 1 : rows <= 32 ? 2 : most;
+  const int64_t per_group = p.few ? 16 * p.row_tiles : head_dim == 256 ? 128 : 256;
   int64_t tiles = (tokens * group + per_group - 1) / per_group;
   if (tiles < batch) tiles = batch;
   const int64_t groups = tiles * kv_heads;
@@ -51,12 +53,161 @@ inline MxAttnPlan mx_attention_plan(int64_t tokens, int64_t batch, int64_t heads
     const int64_t w = window + per_group / group + sinks;
     if (w < seen) seen = w;
   }
-  const int64_t most_splits = seen / (32 * kMinTiles * (p.coop ? 4 : 1));
+  const int64_t most_splits = seen / (32 * kMinTiles * 4);
   int64_t s = groups >= kWanted ? 1 : kWanted / groups;
   if (s > most_splits) s = most_splits;
-  if (s > kMostSplits) s = kMostSplits;
+  if (s > kMxMostSplits) s = kMxMostSplits;
   p.splits = s < 1 ? 1 : (int)s;
   return p;
+}
+
+hipError_t launch_mx_attention_prompt(const MxAttnArgs& a, hipStream_t stream);
+
+// ---- device side ----
+
+constexpr float kMxRaise = 8.0f;  // log2 of how far weights may exceed 1 before the maximum is raised
+
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8_t;
+typedef __attribute__((ext_vector_type(4))) float f32x4_t;
+
+__device__ __forceinline__ bf16x8_t as_bf16x8(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  const u32x4_t w = {a, b, c, d};
+  bf16x8_t r;
+  __builtin_memcpy(&r, &w, 16);
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  bf16x2_t c;
+  c[0] = (__bf16)lo;
+  c[1] = (__bf16)hi;
+  return as_u32(c);
+}
+
+// codes 2 sel, 2 sel + 1 of q as packed bf16
+__device__ __forceinline__ uint32_t decode2(uint32_t q, float s, int sel) {
+  switch (sel) {
+    case 0: return as_u32(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 0));
+    case 1: return as_u32(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 1));
+    case 2: return as_u32(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 2));
+    default: return as_u32(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 3));
+  }
+}
+
+// bits -> eight bf16 that are 1 where the bit is set
+__device__ __forceinline__ bf16x8_t mx_ones(uint32_t bits) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = (bits >> (2 * i) & 1 ? 0x3F80u : 0u) | (bits >> (2 * i + 1) & 1 ? 0x3F800000u : 0u);
+  return as_bf16x8(w[0], w[1], w[2], w[3]);
+}
+
+template <int N>
+struct Words {
+  uint32_t w[N];
+};
+
+template <int N>
+__device__ __forceinline__ Words<N> load_words(const uint8_t* p) {
+  Words<N> r;
+  if constexpr (N == 1) {
+    r.w[0] = *(const uint32_t*)p;
+  } else if constexpr (N == 2) {
+    const u32x2_t v = *(const u32x2_t*)p;
+    r.w[0] = v[0];
+    r.w[1] = v[1];
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const u32x4_t v = *(const u32x4_t*)(p + 16 * i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r.w[4 * i + j] = v[j];
+    }
+  }
+  return r;
+}
+
+// The packed rows of a workgroup: per sequence the (row, head of the group) pairs, group
+// fastest, in tiles of kRows. Sequence i's tiles are numbered from floor(start_i group /
+// kRows) + i: that leaves each at least as many numbers as it has tiles, without a scan of
+// the lengths; numbers without a tile have first >= count.
+struct MxRows {
+  int seq;
+  int64_t r0;     // the sequence's first row in the packed tensors
+  int count;      // packed rows of the sequence
+  int first;      // the tile's first packed row
+  int kv_len;
+  int back;       // position of the sequence's first row
+};
+
+__device__ __forceinline__ MxRows mx_rows(const MxAttnArgs& a, int64_t tile, int rows) {
+  int lo = 0, hi = a.b.batch;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (mx_row_start(a.b, mid) * a.group / rows + mid <= tile) lo = mid;
+    else hi = mid;
+  }
+  MxRows r;
+  const int64_t r1 = mx_row_start(a.b, lo + 1);
+  r.seq = lo;
+  r.r0 = mx_row_start(a.b, lo);
+  r.count = r1 > r.r0 ? (int)((r1 - r.r0) * a.group) : 0;
+  const int64_t first = (tile - (r.r0 * a.group / rows + lo)) * rows;
+  r.first = first < 0 || first > r.count ? r.count : (int)first;
+  r.kv_len = mx_seq_len(a.b, lo);
+  r.back = r.kv_len - (int)(r1 - r.r0);
+  return r;
+}
+
+// What packed rows [p0, p1) of a sequence see: row at position p the tokens [low, high) and
+// those below sinks, with these bounds over the rows.
+struct MxSight {
+  int high_min, high_max, low_min, low_max, sinks;
+};
+
+__device__ __forceinline__ int mx_high(const MxAttnArgs& a, int kv_len, int pos) {
+  const int h = a.causal && pos + 1 < kv_len ? pos + 1 : kv_len;
+  return h > 0 ? h : 0;
+}
+
+__device__ __forceinline__ int mx_low(const MxAttnArgs& a, int pos) {
+  return a.window > 0 && pos - a.window + 1 > 0 ? pos - a.window + 1 : 0;
+}
+
+__device__ __forceinline__ MxSight mx_sight(const MxAttnArgs& a, const MxRows& r, int p0, int p1) {
+  const int pos_a = r.back + p0 / a.group, pos_b = r.back + (p1 - 1) / a.group;
+  return MxSight{mx_high(a, r.kv_len, pos_a), mx_high(a, r.kv_len, pos_b), mx_low(a, pos_a), mx_low(a, pos_b),
+                 a.window > 0 ? a.sinks : 0};
+}
+
+// The tiles of `size` tokens that those rows see: the ones that hold first tokens, then
+// from the window's start (or 0) to the last visible token.
+struct MxSpan {
+  int first, begin, count;  // tiles [0, first), then [begin, ...); count in all
+  __device__ __forceinline__ int at(int i) const { return i < first ? i : begin + (i - first); }
+};
+
+__device__ __forceinline__ MxSpan mx_span(const MxSight& s, int size) {
+  MxSpan t;
+  t.first = ((s.sinks < s.high_max ? s.sinks : s.high_max) + size - 1) / size;
+  t.begin = s.low_min / size > t.first ? s.low_min / size : t.first;
+  const int end = (s.high_max + size - 1) / size;
+  t.count = t.first + (end > t.begin ? end - t.begin : 0);
+  return t;
+}
+
+// the page of token t of sequence seq, or -1
+__device__ __forceinline__ int64_t mx_page(const MxAttnArgs& a, const MxRows& r, int t) {
+  if (t >= r.kv_len) return -1;
+  const int64_t p = a.b.block_table[(int64_t)r.seq * a.b.table_stride + (t >> a.b.page_shift)];
+  return p >= 0 && p < a.b.num_pages ? p : -1;
+}
+
+// first of the cache's rows for 16 tokens from t (a multiple of 16) on that page; a page
+// that is not there is read as page 0, and what is read must not be used
+__device__ __forceinline__ int64_t mx_cache_row(const MxAttnArgs& a, int64_t page, int head, int t) {
+  return (((page < 0 ? 0 : page) * a.c.kv_heads + head) << a.b.page_shift) + (t & ((1 << a.b.page_shift) - 1));
 }
 
 }  // namespace nvfp4
