@@ -15,18 +15,28 @@
 //                  laid in LDS by element with its tokens in that order, again one read.
 //
 // Each wave reads the whole tile from LDS for its 32 RB rows; with 64 rows (RB = 2) that is
-// half of what LDS can deliver in the time of the products. O, Q, two halves' scores and the
-// weights are then about 330 registers: one wave a SIMD, so overlap comes from the
-// instruction stream. A tile goes in two halves of 32 tokens; the scores of the next half
-// are multiplied while this one's exponentials are taken, and the next tile is decoded
-// beside the products with V:
+// half of what LDS can deliver in the time of the products. O, Q, the scores of two halves,
+// the weights and the fragments read ahead are then about 400 registers: one wave a SIMD, so
+// overlap comes from the instruction stream, and every instruction counts. A tile goes in
+// two halves of 32 tokens, each in two phases of 2 D / 16 matrix instructions beside what
+// else is due:
 //
-//   barrier | S1 = K[t]1 Q     ||  P = exp2(S0) | O += V[t]0 P  ||  decode K[t + 1]
-//   barrier | S0 = K[t + 1]0 Q ||  P = exp2(S1) | O += V[t]1 P  ||  decode V[t + 1]
+//   1  S1 = K[t]1 Q       ||  P = exp2(S0)                  ||  read V[t]0
+//   2  O += V[t]0 P       ||  decode V[t + 1] into LDS      ||  read K[t + 1]0   | barrier
+//   3  S0 = K[t + 1]0 Q   ||  P = exp2(S1)                  ||  read V[t]1
+//   4  O += V[t]1 P       ||  decode K[t + 2] into LDS      ||  read K[t + 1]1   | barrier
 //
-// Masks are put into S as -inf, only in tiles that some row does not see whole. Arithmetic
-// and the raising of the maximum are those of mx_attn.hip.
+// Weights are taken under the maximum as it stands, and their sum, which is needed anyway,
+// tells afterwards whether a score exceeded it by too much: then the maximum is raised and
+// the half's weights are taken again. So most halves look for no maximum at all. The sum is
+// of the weights as rounded for the product, two to an instruction (v_dot2_f32_bf16, fp32).
+//
+// Masks are put into S as -inf, only in halves that some row does not see whole. Arithmetic
+// is that of mx_attn.hip.
+#include <type_traits>
+
 #include "mx_attn.hpp"
+
 
 namespace nvfp4 {
 
@@ -35,23 +45,25 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kTile = 64;  // tokens per step: 16 to a wave when they are decoded
 
-// position of 16-byte chunk c of K row t (D / 8 chunks) and of V row d (8 chunks): the 16
-// rows that a read phase meets lie in different banks
-template <int D>
-__device__ __forceinline__ int k_chunk(int t, int c) {
-  return c ^ (D == 64 ? (t >> 1) & 7 : t & 15);
-}
+// A raise is due when the weights of a lane's 16 tokens add up to more: some weight is then
+// above 2^8, and none that passes is above 2^12.
+constexpr float kMostSum = 4096.0f;
+
+// K rows are padded by 16 bytes; in V rows (64 tokens, 8 chunks of 16 bytes) chunk c lies at
+// v_chunk: either way the 16 rows that a read phase meets lie in different banks
 __device__ __forceinline__ int v_chunk(int d, int c) { return c ^ (((d >> 1) ^ (d >> 3)) & 7); }
 
 template <int D>
 struct Lds {
-  static constexpr int K = kTile * D * 2, V = D * kTile * 2;  // bytes of a tile
+  static constexpr int KRow = D * 2 + 16;
+  static constexpr int K = kTile * KRow, V = D * kTile * 2;   // bytes of a tile
   static constexpr int Nan = D / 32 * kTile;                  // V bytes that are NaN, [block][token]
   static constexpr int VAt = 2 * K, NanAt = VAt + 2 * V, FlagAt = NanAt + 2 * Nan, Bytes = FlagAt + 2 * 4 * kWaves;
+  static_assert(Bytes <= 160 * 1024, "LDS");
 };
 
 template <int D, int RB>
-__global__ __launch_bounds__(64 * kWaves, 1) void mx_attention_prompt_kernel(MxAttnArgs a) {
+__global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : 1) void mx_attention_prompt_kernel(MxAttnArgs a) {
   using L = Lds<D>;
   constexpr int KS = D / 16, DB = D / 32;
   constexpr int kRows = 32 * RB * kWaves;
@@ -106,70 +118,94 @@ __global__ __launch_bounds__(64 * kWaves, 1) void mx_attention_prompt_kernel(MxA
     uint32_t ks[D == 256 ? 2 : 1];
     uint32_t v[4][D == 256 ? 2 : 1];
     uint32_t vs[4];
-    bool there;  // V's page exists
   };
-  auto load_k = [&](Raw& x, int tile) __attribute__((always_inline)) {
-    const int t = tile * kTile + wave * 16;
-    const int64_t row = mx_cache_row(a, mx_page(a, rows, t), kvh, t) + kt;
-    x.k = load_words<D / 32>(a.c.k_codes + row * (D / 2) + kq * (D / 8));
-    const uint8_t* s = a.c.k_scales + row * (D / 32) + kq * (D / 4) / 32;
+  // The block table, 64 entries at a time, one a lane. Of a tile: the cache row of the wave's
+  // 16 tokens (on page 0 if their page is not there) and which of the four 16-token groups
+  // have a page.
+  struct Pages {
+    int64_t row;
+    uint32_t there;
+  };
+  const int32_t* table = a.b.block_table + (int64_t)rows.seq * a.b.table_stride;
+  const int pages = (rows.kv_len + (1 << a.b.page_shift) - 1) >> a.b.page_shift;
+  int entry = 0, base = -64;
+  bool holes = false;  // among the 64
+  auto pages_of = [&](int tile) __attribute__((always_inline)) {
+    const int t = tile * kTile, first = t >> a.b.page_shift, last = (t + 48) >> a.b.page_shift;
+    if ((first < base) | (last >= base + 64)) {  // uniform
+      base = first;
+      entry = first + lane < pages ? table[first + lane] : 0;  // past the last page: never seen
+      if (entry >= a.b.num_pages) entry = -1;
+      holes = __any(entry < 0);
+    }
+    Pages x;
+    x.there = 15u;
+    if (holes) {
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        if (__builtin_amdgcn_readlane(entry, ((t + 16 * w) >> a.b.page_shift) - base) < 0) x.there &= ~(1u << w);
+    }
+    x.row = mx_cache_row(a, __builtin_amdgcn_readlane(entry, ((t + 16 * wave) >> a.b.page_shift) - base), kvh,
+                         t + 16 * wave);
+    return x;
+  };
+  auto load_k = [&](Raw& x, const Pages& pg) __attribute__((always_inline)) {
+    x.k = load_words<D / 32>(a.c.k_codes + pg.row * (D / 2) + (kt * (D / 2) + kq * (D / 8)));
+    const uint8_t* s = a.c.k_scales + pg.row * (D / 32) + (kt * (D / 32) + kq * (D / 4) / 32);
 #pragma unroll
     for (int b = 0; b < (D == 256 ? 2 : 1); ++b) x.ks[b] = s[b];
   };
-  auto load_v = [&](Raw& x, int tile) __attribute__((always_inline)) {
-    const int t = tile * kTile + wave * 16;
-    const int64_t page = mx_page(a, rows, t), row = mx_cache_row(a, page, kvh, t) + 4 * vq;
-    x.there = page >= 0;
+  auto load_v = [&](Raw& x, const Pages& pg) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint8_t* p = a.c.v_codes + (row + i) * (D / 2) + vc * (D / 32);
+      const uint8_t* p = a.c.v_codes + pg.row * (D / 2) + ((4 * vq + i) * (D / 2) + vc * (D / 32));
       if constexpr (D == 64) x.v[i][0] = *(const uint16_t*)p;
       else {
         const Words<D / 128> w = load_words<D / 128>(p);
 #pragma unroll
         for (int j = 0; j < D / 128; ++j) x.v[i][j] = w.w[j];
       }
-      x.vs[i] = a.c.v_scales[(row + i) * (D / 32) + vblk];
+      x.vs[i] = (a.c.v_scales + pg.row * (D / 32))[(4 * vq + i) * (D / 32) + vblk];
     }
   };
-  auto store_k = [&](const Raw& x, int buf) __attribute__((always_inline)) {
-    uint8_t* dst = smem + buf * L::K + (wave * 16 + kt) * (D * 2);
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) {
-      const u32x4_t w = mx_decode8(x.k.w[e], __uint_as_float(x.ks[D == 256 ? e >> 2 : 0] << 23));
-      *(u32x4_t*)(dst + k_chunk<D>(wave * 16 + kt, kq * (D / 32) + e) * 16) = w;
-    }
+  auto store_k = [&](const Raw& x, int buf, int e) __attribute__((always_inline)) {  // piece e of D / 32
+    uint8_t* dst = smem + buf * L::K + (wave * 16 + kt) * L::KRow + kq * (D / 2);
+    *(u32x4_t*)(dst + e * 16) = mx_decode8(x.k.w[e], __uint_as_float(x.ks[D == 256 ? e >> 2 : 0] << 23));
   };
   // V by element. The products must not meet a NaN: 0 * NaN would reach rows that do not
   // see it. NaN blocks go in as zeros (scale 0) and are marked; tokens past the last and on
   // pages that are not there may hold anything and go in under scale 0 too.
-  auto store_v = [&](const Raw& x, int buf, int tile) __attribute__((always_inline)) {
-    uint8_t* dst = smem + L::VAt + buf * L::V;
-    const int t = tile * kTile + wave * 16 + 4 * vq;
-    float s[4];
-    uint32_t marks = 0;
+  auto mark_v = [&](Raw& x, int buf, int tile, const Pages& pg) __attribute__((always_inline)) {
+    const int t0 = tile * kTile + wave * 16;
+    if ((t0 + 16 > rows.kv_len) | ((pg.there >> wave & 1u) == 0)) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool nan = x.vs[i] == 255u, token = x.there && t + i < rows.kv_len;
-      if (nan && token) marks |= 1u << (8 * i);
-      s[i] = __uint_as_float(nan || !token ? 0u : x.vs[i] << 23);
+      for (int i = 0; i < 4; ++i)
+        x.vs[i] = ((t0 + 4 * vq + i < rows.kv_len) & ((pg.there >> wave & 1u) != 0)) ? x.vs[i] : 0u;
     }
-    if ((vc & (16 / DB - 1)) == 0) *(uint32_t*)(smem + L::NanAt + buf * L::Nan + vblk * kTile + wave * 16 + 4 * vq) = marks;
-    const uint64_t any = __ballot(marks != 0);
-    if (lane == 0) *(uint32_t*)(smem + L::FlagAt + (buf * kWaves + wave) * 4) = any != 0;
+    const uint32_t most = max(max(x.vs[0], x.vs[1]), max(x.vs[2], x.vs[3]));
+    const uint32_t any = __any(most == 255u);
+    if (any) {
+      uint32_t marks = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        marks |= x.vs[i] == 255u ? 1u << (8 * i) : 0u;
+        x.vs[i] = x.vs[i] == 255u ? 0u : x.vs[i];
+      }
+      *(uint32_t*)(smem + L::NanAt + buf * L::Nan + vblk * kTile + wave * 16 + 4 * vq) = marks;  // the same from a block's lanes
+    }
+    *(uint32_t*)(smem + L::FlagAt + (buf * kWaves + wave) * 4) = any;
+  };
+  auto store_v = [&](const Raw& x, int buf, int d) __attribute__((always_inline)) {  // elements 2 d, 2 d + 1 of the lane's
     // tokens 4 vq .. + 3 of the 16: lane half vq & 1, first or second four
-    const int c = 2 * wave + (vq & 1), off = (vq >> 1) * 8;
+    uint8_t* dst = smem + L::VAt + buf * L::V + (vq >> 1) * 8;
+    const int c = 2 * wave + (vq & 1), e = vc * (D / 16) + 2 * d;
+    uint32_t two[4];
 #pragma unroll
-    for (int d = 0; d < D / 32; ++d) {  // elements 2 d, 2 d + 1 of the lane's
-      uint32_t two[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) two[i] = decode2(x.v[i][D == 256 ? d >> 2 : 0], s[i], d & 3);
-      const int e = vc * (D / 16) + 2 * d;
-      *(u32x2_t*)(dst + e * 128 + v_chunk(e, c) * 16 + off) =
-          u32x2_t{__builtin_amdgcn_perm(two[1], two[0], 0x05040100u), __builtin_amdgcn_perm(two[3], two[2], 0x05040100u)};
-      *(u32x2_t*)(dst + (e + 1) * 128 + v_chunk(e + 1, c) * 16 + off) =
-          u32x2_t{__builtin_amdgcn_perm(two[1], two[0], 0x07060302u), __builtin_amdgcn_perm(two[3], two[2], 0x07060302u)};
-    }
+    for (int i = 0; i < 4; ++i) two[i] = decode2(x.v[i][D == 256 ? d >> 2 : 0], __uint_as_float(x.vs[i] << 23), d & 3);
+    *(u32x2_t*)(dst + e * 128 + v_chunk(e, c) * 16) =
+        u32x2_t{__builtin_amdgcn_perm(two[1], two[0], 0x05040100u), __builtin_amdgcn_perm(two[3], two[2], 0x05040100u)};
+    *(u32x2_t*)(dst + (e + 1) * 128 + v_chunk(e + 1, c) * 16) =
+        u32x2_t{__builtin_amdgcn_perm(two[1], two[0], 0x07060302u), __builtin_amdgcn_perm(two[3], two[2], 0x07060302u)};
   };
 
   // ---- state ----
@@ -185,27 +221,25 @@ __global__ __launch_bounds__(64 * kWaves, 1) void mx_attention_prompt_kernel(MxA
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[r][d][i] = 0.0f;
   }
+  bool fresh = true;  // some row has seen nothing yet
 
-  auto scores = [&](f32x16_t (&x)[RB], int buf, int half) __attribute__((always_inline)) {
-    const uint8_t* src = smem + buf * L::K;
-    const int t = half * 32 + n;
+  bf16x8_t kf[KS], vf[KS];  // fragments of a half: K by step, V by (16 tokens, block)
+  auto read_k = [&](int buf, int half, int k) __attribute__((always_inline)) {
+    kf[k] = *(const bf16x8_t*)(smem + buf * L::K + (half * 32 + n) * L::KRow + h * 16 + k * 32);
+  };
+  auto read_v = [&](int buf, int half, int k) __attribute__((always_inline)) {
+    const int e = k % DB * 32 + n;
+    vf[k] = *(const bf16x8_t*)(smem + L::VAt + buf * L::V + e * 128 + v_chunk(e, 4 * half + 2 * (k / DB) + h) * 16);
+  };
+  auto zero = [&](f32x16_t (&x)[RB]) __attribute__((always_inline)) {
 #pragma unroll
     for (int r = 0; r < RB; ++r)
 #pragma unroll
       for (int i = 0; i < 16; ++i) x[r][i] = 0.0f;
-#pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      const bf16x8_t kf = *(const bf16x8_t*)(src + t * (D * 2) + k_chunk<D>(t, 2 * k + h) * 16);
-#pragma unroll
-      for (int r = 0; r < RB; ++r) x[r] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, q[r][k], x[r], 0, 0, 0);
-    }
   };
-  // which 16-token groups of the tile have a page
-  auto there_of = [&](int tile) __attribute__((always_inline)) {
-    uint32_t there = 0;
+  auto scores = [&](f32x16_t (&x)[RB], int k) __attribute__((always_inline)) {  // step k
 #pragma unroll
-    for (int w = 0; w < 4; ++w) there |= mx_page(a, rows, tile * kTile + 16 * w) >= 0 ? 1u << w : 0u;
-    return there;
+    for (int r = 0; r < RB; ++r) x[r] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[k], q[r][k], x[r], 0, 0, 0);
   };
   // (no short-circuits: selects, not branches around the accumulators)
   auto sees = [&](int r, int t, uint32_t there, int group) __attribute__((always_inline)) {
@@ -223,63 +257,96 @@ __global__ __launch_bounds__(64 * kWaves, 1) void mx_attention_prompt_kernel(MxA
       for (int i = 0; i < 16; ++i)
         x[r][i] = sees(r, t0 + 8 * (i >> 2) + 4 * h + (i & 3), there, 2 * half + (i >> 3)) ? x[r][i] : -INFINITY;
   };
-  auto raise = [&](const f32x16_t (&x)[RB]) __attribute__((always_inline)) {
-    float top[RB];
-    bool need = false;
-#pragma unroll
-    for (int r = 0; r < RB; ++r) {
-      top[r] = x[r][0];
-#pragma unroll
-      for (int i = 1; i < 16; ++i) top[r] = fmaxf(top[r], x[r][i]);
-      top[r] *= a.scale_log2;
-      need |= top[r] > m[r] + kMxRaise;
-    }
-    if (!__any(need)) return;
-#pragma unroll
-    for (int r = 0; r < RB; ++r) {
-      const float next = fmaxf(m[r], fmaxf(top[r], __shfl_xor(top[r], 32, 64)));
-      const float f = m[r] == next ? 1.0f : __builtin_amdgcn_exp2f(m[r] - next);  // m = -inf: o and l are 0
-      m[r] = next;
-      l[r] *= f;
-#pragma unroll
-      for (int d = 0; d < DB; ++d) o[r][d] *= f;
-    }
-  };
   bf16x8_t pf[RB][2];
-  auto weights = [&](const f32x16_t (&x)[RB]) __attribute__((always_inline)) {
+  uint32_t pw[RB][8];  // the weights, packed
+  float sum[RB];       // of the lane's 16
+  // weights 4 j .. 4 j + 3 of row block j / 4: taken (the exponentials), then summed and packed
+  auto take = [&](const f32x16_t (&x)[RB], int j, float (&p)[4]) __attribute__((always_inline)) {
+    const int r = j >> 2;
+    const float neg = m[r] == -INFINITY ? 0.0f : -m[r];  // nothing seen yet: every weight is exp2(-inf)
 #pragma unroll
-    for (int r = 0; r < RB; ++r) {
-      const float neg = m[r] == -INFINITY ? 0.0f : -m[r];  // nothing seen yet: every weight is exp2(-inf)
+    for (int i = 0; i < 4; ++i) p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[r][4 * (j & 3) + i], a.scale_log2, neg));
+  };
+  auto add = [&](int j, const float (&p)[4]) __attribute__((always_inline)) {
+    const int r = j >> 2;
+    const uint32_t w0 = pack_bf16(p[0], p[1]), w1 = pack_bf16(p[2], p[3]);
+    const bf16x2_t one = as_bf16x2(0x3F803F80u);
+    const float t = __builtin_amdgcn_fdot2_f32_bf16(as_bf16x2(w0), one, (j & 3) == 0 ? 0.0f : sum[r], false);
+    sum[r] = __builtin_amdgcn_fdot2_f32_bf16(as_bf16x2(w1), one, t, false);
+    pw[r][2 * (j & 3)] = w0;
+    pw[r][2 * (j & 3) + 1] = w1;
+  };
+  // after the weights of x: raises the maximum and takes them again if that is due
+  auto settle = [&](const f32x16_t (&x)[RB]) __attribute__((always_inline)) {
+    bool due = fresh;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float p[8];
+    for (int r = 0; r < RB; ++r) due |= !(sum[r] <= kMostSum);
+    if (__any(due)) {
+      bool none = false;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[r][8 * k + i], a.scale_log2, neg));
-        l[r] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
-        pf[r][k] = as_bf16x8(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7]));
+      for (int r = 0; r < RB; ++r) {
+        float top = x[r][0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) top = fmaxf(top, x[r][i]);
+        top *= a.scale_log2;
+        const float next = fmaxf(m[r], fmaxf(top, __shfl_xor(top, 32, 64)));
+        const float f = m[r] == next ? 1.0f : __builtin_amdgcn_exp2f(m[r] - next);  // m = -inf: o and l are 0
+        m[r] = next;
+        none |= (next == -INFINITY) & (high[r] > 0);
+        l[r] *= f;
+#pragma unroll
+        for (int d = 0; d < DB; ++d) o[r][d] *= f;
+      }
+      fresh = __any(none);
+#pragma unroll
+      for (int j = 0; j < 4 * RB; ++j) {
+        float p[4];
+        take(x, j, p);
+        add(j, p);
       }
     }
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      l[r] += sum[r];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) pf[r][k] = as_bf16x8(pw[r][4 * k], pw[r][4 * k + 1], pw[r][4 * k + 2], pw[r][4 * k + 3]);
+    }
   };
-  auto values = [&](int buf, int half) __attribute__((always_inline)) {
-    const uint8_t* src = smem + L::VAt + buf * L::V;
+  auto values = [&](int k) __attribute__((always_inline)) {  // 16 tokens k / DB, block k % DB
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+    for (int r = 0; r < RB; ++r)
+      o[r][k % DB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[k], pf[r][k / DB], o[r][k % DB], 0, 0, 0);
+  };
+  // The phases, in steps of RB matrix instructions each with its share of the rest, fenced so
+  // that the order stands: left alone the instructions gather by kind, and one wave a SIMD
+  // then does first the one and then the other.
+  auto fence = []() __attribute__((always_inline)) { __builtin_amdgcn_sched_barrier(0); };
+  auto phase_scores = [&](f32x16_t (&x)[RB], const f32x16_t (&y)[RB], int vbuf, int half) __attribute__((always_inline)) {
+    constexpr int G = 4 * RB;  // groups of weights, over KS steps; packed a step after they are taken
+    float p[2][4];
+    zero(x);
 #pragma unroll
-      for (int d = 0; d < DB; ++d) {
-        const int e = d * 32 + n;
-        const bf16x8_t vf = *(const bf16x8_t*)(src + e * 128 + v_chunk(e, 4 * half + 2 * k + h) * 16);
+    for (int k = 0; k < KS; ++k) {
+      scores(x, k);
+      read_v(vbuf, half, k);
 #pragma unroll
-        for (int r = 0; r < RB; ++r) o[r][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[r][k], o[r][d], 0, 0, 0);
+      for (int j = k * G / KS; j < (k + 1) * G / KS; ++j) {
+        if (j > 0) add(j - 1, p[(j - 1) & 1]);
+        take(y, j, p[j & 1]);
       }
+      fence();
+    }
+    add(G - 1, p[(G - 1) & 1]);
   };
+
   // Marked blocks: a product of "is NaN" with "is seen" tells the rows that get one, for the
   // whole block of 32 elements at once.
-  auto nans = [&](int buf, int tile) __attribute__((always_inline)) {
-    const u32x4_t flag = *(const u32x4_t*)(smem + L::FlagAt + buf * kWaves * 4);
+  u32x4_t flag;  // of V[t], one word a wave
+  auto nans = [&](int buf, int tile, uint32_t there) __attribute__((always_inline)) {
     if (__builtin_amdgcn_readfirstlane(flag[0] | flag[1] | flag[2] | flag[3]) == 0) return;
-    const uint32_t there = there_of(tile);
-#pragma nounroll
-    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {  // wave k's tokens
+      if (__builtin_amdgcn_readfirstlane(flag[k]) == 0) continue;
       bf16x8_t seen[RB];
 #pragma unroll
       for (int r = 0; r < RB; ++r) {
@@ -321,41 +388,79 @@ __global__ __launch_bounds__(64 * kWaves, 1) void mx_attention_prompt_kernel(MxA
   if (begin < end) {
     Raw x;
     auto clamp = [&](int i) __attribute__((always_inline)) { return span.at(i < end ? i : end - 1); };
-    int tile = span.at(begin);
-    uint32_t there = there_of(tile);
-    load_k(x, tile);
-    load_v(x, tile);
-    store_k(x, 0);
-    store_v(x, 0, tile);
-    load_k(x, clamp(begin + 1));
-    load_v(x, clamp(begin + 1));
+    int tile = span.at(begin), next = clamp(begin + 1), far = clamp(begin + 2);
+    Pages at = pages_of(tile), an = pages_of(next), af = pages_of(far);  // of the three tiles
+    load_k(x, at);
+    load_v(x, at);
+#pragma unroll
+    for (int d = 0; d < DB; ++d) store_k(x, 0, d);
+    mark_v(x, 0, tile, at);
+#pragma unroll
+    for (int d = 0; d < DB; ++d) store_v(x, 0, d);
+    load_k(x, an);
+#pragma unroll
+    for (int d = 0; d < DB; ++d) store_k(x, 1, d);
+    load_v(x, an);
+    load_k(x, af);
     barrier();
-    scores(s0, 0, 0);
-    mask(s0, tile, 0, there);
-    int buf = 0;
-    for (int i = begin; i < end; ++i) {
-      const int next = clamp(i + 1);
-      // V[i] is in LDS; no wave reads K[i - 1] or V[i - 1] any more
-      if (i > begin) barrier();
-      nans(buf, tile);
-      raise(s0);
-      scores(s1, buf, 1);
-      weights(s0);
-      values(buf, 0);
-      store_k(x, buf ^ 1);
-      load_k(x, clamp(i + 2));
-      mask(s1, tile, 1, there);
-      barrier();  // K[i + 1] is in LDS
-      raise(s1);
-      there = there_of(next);
-      scores(s0, buf ^ 1, 0);
-      weights(s1);
-      values(buf, 1);
-      store_v(x, buf ^ 1, next);
-      load_v(x, clamp(i + 2));
-      mask(s0, next, 0, there);
+    zero(s0);
+#pragma unroll
+    for (int k = 0; k < KS; ++k) read_k(0, 0, k);
+#pragma unroll
+    for (int k = 0; k < KS; ++k) scores(s0, k);
+    mask(s0, tile, 0, at.there);
+#pragma unroll
+    for (int k = 0; k < KS; ++k) read_k(0, 1, k);
+    flag = *(const u32x4_t*)(smem + L::FlagAt);
+    auto body = [&](int i, auto buffer) __attribute__((always_inline)) {
+      constexpr int buf = decltype(buffer)::value;
+      nans(buf, tile, at.there);
+      const int beyond = clamp(i + 3);
+      const Pages ab = pages_of(beyond);
+      // 1
+      fence();
+      phase_scores(s1, s0, buf, 0);
+      settle(s0);
+      mask(s1, tile, 1, at.there);
+      // 2
+      fence();
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        values(k);
+        read_k(buf ^ 1, 0, k);
+        if (k == 0) mark_v(x, buf ^ 1, next, an);
+        if (k & 1) store_v(x, buf ^ 1, k >> 1);
+        fence();
+      }
+      load_v(x, af);
+      barrier();
+      // 3
+      flag = *(const u32x4_t*)(smem + L::FlagAt + (buf ^ 1) * kWaves * 4);
+      fence();
+      phase_scores(s0, s1, buf, 1);
+      settle(s1);
+      mask(s0, next, 0, an.there);
+      // 4
+      fence();
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        values(k);
+        read_k(buf ^ 1, 1, k);
+        if (k & 1) store_k(x, buf, k >> 1);
+        fence();
+      }
+      load_k(x, ab);
+      barrier();
       tile = next;
-      buf ^= 1;
+      next = far;
+      far = beyond;
+      at = an;
+      an = af;
+      af = ab;
+    };
+    for (int i = begin; i < end; i += 2) {
+      body(i, std::integral_constant<int, 0>());
+      if (i + 1 < end) body(i + 1, std::integral_constant<int, 1>());
     }
   }
 
