@@ -12,8 +12,8 @@
 // What bounds it is reading the cache: every visible token once per kv head, 17/32 bytes an
 // element. A wave moves its codes and scales to a ring of its own in LDS, 32 tokens a slot,
 // with direct-to-LDS loads that need no register while they fly and no barrier (five
-// instructions for 32 tokens of 128 elements, every one of whole runs), kRing slots ahead:
-// 8 waves x 4 slots x 4.25 KiB in flight per CU.
+// instructions for 32 tokens of 128 elements, every one of whole runs): 16 waves x 2 slots
+// x 4.25 KiB in flight per CU.
 //
 // One pass with the running maximum and sum of the softmax, in the transposed form with
 // v_mfma_f32_16x16x32_bf16, lane (n, u) = (lane & 15, lane >> 4):
@@ -31,8 +31,8 @@
 // Packed row n stays in the lanes n + 16 u from the scores to the output, and lane (n, u)
 // ends with elements [u D/4, (u + 1) D/4) of its row. Codes become exact bf16
 // (v_cvt_scalef32_pk_bf16_fp4); scores, maxima, sums and o are fp32. P is rounded to bf16
-// for the product (2^-8 of each weight at most, the size of o's own rounding); its sum takes
-// the unrounded weights.
+// for the product (2^-8 of each weight at most, the size of o's own rounding); its sum is of
+// the same rounded weights, so that they still add up to one.
 //
 // The maximum is raised only when a score exceeds it by more than 2^8: until then weights
 // up to 2^8 are as exact as those below 1, and most tiles skip the cross-lane maximum and
@@ -58,8 +58,14 @@ struct Slot {
   static constexpr int CodeLoads = Codes / 1024;                  // 16 bytes a lane, of K and of V
   static constexpr int ScaleLoads = (2 * Scales + 255) / 256;     // a dword a lane, of both
   static constexpr int Loads = 2 * CodeLoads + ScaleLoads;
-  static constexpr int Ring = D == 64 ? 8 : D == 128 ? 4 : 2;     // about 70 KiB for four waves
 };
+
+// Workgroups of a CU, by registers, and the ring slots of a wave that then fit: 34 KiB for a
+// workgroup of four waves, or 68 KiB. Measured on 48 single tokens over up to 8200 (D 128,
+// RT 1): four workgroups with 2 slots 92 us, three with 3 slots 103, two with 4 slots 120 -
+// more waves hide more than more slots.
+constexpr int groups_per_cu(int d, int rt) { return d * rt <= 128 ? (rt == 1 ? 4 : 3) : d * rt <= 256 ? 2 : 1; }
+constexpr int ring_slots(int d, int rt) { return (d * rt <= 128 ? 256 : 512) / d; }
 
 template <int N>
 __device__ __forceinline__ void wait_loads() {  // vmcnt(N)
@@ -69,9 +75,9 @@ __device__ __forceinline__ void wait_loads() {  // vmcnt(N)
 }
 
 template <int D, int RT>
-__global__ __launch_bounds__(64 * kWaves, D * RT > 256 ? 1 : 2) void mx_attention_few_kernel(MxAttnArgs a) {
+__global__ __launch_bounds__(64 * kWaves, groups_per_cu(D, RT)) void mx_attention_few_kernel(MxAttnArgs a) {
   using S = Slot<D>;
-  constexpr int NJ = D / 16, KS = D / 32, E = D / 4, R = S::Ring;
+  constexpr int NJ = D / 16, KS = D / 32, E = D / 4, R = ring_slots(D, RT);
   constexpr int kRows = 16 * RT;  // packed rows of the workgroup
   constexpr int kRed = kWaves * E * 64 * 4;
   constexpr int kLds = kWaves * R * S::Bytes > kRed ? kWaves * R * S::Bytes : kRed;
@@ -133,13 +139,14 @@ __global__ __launch_bounds__(64 * kWaves, D * RT > 256 ? 1 : 2) void mx_attentio
   auto load = [&](int slot, int tile) __attribute__((always_inline)) {
     const int t0 = tile * kTile;
     int64_t row[2];
-    uint32_t there = 0;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int t = t0 + 16 * h;
-      const int page = t < rows.kv_len ? page_of(t) : -1;
-      if (page >= 0) there |= 1u << h;
-      row[h] = mx_cache_row(a, page, kvh, t);
+    int page = page_of(t0);  // of a token that some row sees
+    uint32_t there = page >= 0 ? 3u : 0u;
+    row[0] = mx_cache_row(a, page, kvh, t0);
+    row[1] = row[0] + 16;
+    if (a.b.page_shift == 4) {  // else the halves share a page
+      page = t0 + 16 < rows.kv_len ? page_of(t0 + 16) : -1;
+      there = (there & 1u) | (page >= 0 ? 2u : 0u);
+      row[1] = mx_cache_row(a, page, kvh, t0 + 16);
     }
     there_bits = (there_bits & ~(3u << (2 * slot))) | (there << (2 * slot));
     uint8_t* dst = ring + slot * S::Bytes;
@@ -230,12 +237,16 @@ __global__ __launch_bounds__(64 * kWaves, D * RT > 256 ? 1 : 2) void mx_attentio
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         p[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][j >> 2][j & 3], a.scale_log2, neg));
-      l[r] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
-      pf[r] = as_bf16x8(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7]));
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        w[j] = pack_bf16(p[2 * j], p[2 * j + 1]);
+        l[r] = __builtin_amdgcn_fdot2_f32_bf16(as_bf16x2(w[j]), as_bf16x2(0x3F803F80u), l[r], false);
+      }
+      pf[r] = as_bf16x8(w[0], w[1], w[2], w[3]);
     }
     uint32_t vc[8][D == 256 ? 2 : 1];
     float vs[8];
-    uint32_t nans = 0;  // bit j: the lane's block of its token j is NaN
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int t = 4 * u + (j & 3);
@@ -246,9 +257,7 @@ __global__ __launch_bounds__(64 * kWaves, D * RT > 256 ? 1 : 2) void mx_attentio
 #pragma unroll
         for (int k = 0; k < D / 128; ++k) vc[j][k] = w.w[k];
       }
-      const uint32_t byte = x[S::VS + (j >> 2) * S::SHalf + t * (D / 32) + vblk];
-      if (byte == 255u) nans |= 1u << j;
-      vs[j] = __uint_as_float(byte << 23);
+      vs[j] = __uint_as_float((uint32_t)x[S::VS + (j >> 2) * S::SHalf + t * (D / 32) + vblk] << 23);
     }
     // 0 * NaN is NaN, and a row must not meet a NaN that it does not see (another row's
     // token, or what lies behind the last one): where not all rows see all, NaN blocks leave
@@ -256,12 +265,13 @@ __global__ __launch_bounds__(64 * kWaves, D * RT > 256 ? 1 : 2) void mx_attentio
     // tells the rows that get one. The lane's elements all lie in one block, so its answer
     // holds for all of them.
     // Tokens that no row sees may hold anything, infinite values too: their scale becomes 0.
+    uint32_t nans = 0;  // bit j: the lane's block of its token j is NaN
     if (!full) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const bool none = (t0 + 16 * (j >> 2) + 4 * u + (j & 3) >= sight.high_max) | ((there >> (j >> 2) & 1u) == 0);
         vs[j] = none ? 0.0f : vs[j];
-        nans = none ? nans & ~(1u << j) : nans;
+        nans |= __float_as_uint(vs[j]) == 255u << 23 ? 1u << j : 0u;
       }
     }
     if (!full && __any(nans != 0)) {
@@ -420,11 +430,15 @@ __global__ __launch_bounds__(256) void mx_attention_join_kernel(MxAttnArgs a) {
   const float sum = all(v.y == 0.0f ? 0.0f : f * v.y, false);
   if (tid < a.splits) weight[tid] = v.y == 0.0f ? -1.0f : f;
   __syncthreads();
+  // what a split that saw nothing left there is read and not used
   f32x4_t y = {0.0f, 0.0f, 0.0f, 0.0f};
+  const float* src = a.part_o + pair * D + (tid % L) * 4;
+#pragma unroll 8
   for (int s = tid / L; s < a.splits; s += P) {
     const float w = weight[s];
-    if (w == -1.0f) continue;
-    y += w * *(const f32x4_t*)(a.part_o + (s * pairs + pair) * D + (tid % L) * 4);
+    const f32x4_t o = *(const f32x4_t*)(src + s * pairs * D);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] += w == -1.0f ? 0.0f : w * o[i];
   }
   part[tid] = y;
   __syncthreads();

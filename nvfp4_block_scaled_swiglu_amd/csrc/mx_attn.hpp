@@ -31,12 +31,15 @@ struct MxAttnPlan {
 // Rows: the packed rows (rows x heads of a group) of an average sequence. Up to 64 of them
 // (32 at head_dim 256) are one workgroup's of the few-rows form, whose four waves split the
 // tokens; beyond that the prompt form gives every wave rows of its own.
-// Splits: enough workgroups to fill 256 CUs four times where the rows alone do not, but
-// at least kMinTiles 32-token tiles a wave, so that a split is more than its own start
-// and its share of the join.
+// Splits: where the rows alone do not give enough workgroups, pieces of the token axis do,
+// but at least kMinTiles 32-token tiles a wave, so that a split is more than its own start
+// and its share of the join. Few rows: 8 workgroups for each of the 256 CUs (ragged lengths
+// then even out over two rounds of them: 48 tokens over up to 8200 take 92 us with 5 splits,
+// 108 with 2, 97 with 8). Prompts: their workgroups are long and one fills a CU, and a split
+// writes and reads every row once more in fp32, so only what leaves CUs idle is split.
 inline MxAttnPlan mx_attention_plan(int64_t tokens, int64_t batch, int64_t heads, int64_t kv_heads, int64_t head_dim,
                                     int64_t max_kv, int64_t window, int64_t sinks) {
-  constexpr int64_t kWanted = 1024, kMinTiles = 2;
+    constexpr int64_t kMinTiles = 2;
   MxAttnPlan p{true, 1, 1};
   if (tokens <= 0 || batch <= 0) return p;
   const int64_t group = heads / kv_heads;
@@ -54,7 +57,7 @@ inline MxAttnPlan mx_attention_plan(int64_t tokens, int64_t batch, int64_t heads
     if (w < seen) seen = w;
   }
   const int64_t most_splits = seen / (32 * kMinTiles * 4);
-  int64_t s = groups >= kWanted ? 1 : kWanted / groups;
+  int64_t s = p.few ? 2048 / groups : 256 / groups;
   if (s > most_splits) s = most_splits;
   if (s > kMxMostSplits) s = kMxMostSplits;
   p.splits = s < 1 ? 1 : (int)s;
