@@ -26,6 +26,7 @@ struct MxGemmArgs {
   int64_t ldd, m, n, k;
   int groups;            // scale columns / 4 = K steps of 128
   int tiles_m, tiles_n;
+  int whole, parts;      // tiles [0, whole) are run whole, the rest in this many parts
   bool wide;             // D rows take 16-byte stores
 };
 
@@ -41,32 +42,36 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 // ---- tiles ---------------------------------------------------------------------------------
-// A workgroup of 4 waves (2 x 2) computes (64 FM) x (64 FN); a wave owns FM x FN tiles of
+// A workgroup of 4 waves (2 x 2) computes (64 FM) x (64 FN), FM = FN = 4 for whole tiles; a wave owns FM x FN tiles of
 // 32 x 32. K advances 128 per step: 64 code bytes a row and one 512-byte scale tile per
 // 128 rows. Direct-to-LDS loads bring step ks + kStages while step ks is multiplied.
 // A step has two halves of one MFMA per tile each: while the MFMAs of a half run, the
-// fragments of the next are read from LDS. The barrier sits between the halves: every wave
-// has then read both halves of step ks, whose stage takes the next loads, and each has
-// seen its own loads of step ks + 1 land.
+// fragments of the next are read from LDS, in a fixed order of fenced steps (left alone they
+// gather in front of the MFMAs that use them, and one wave a SIMD waits for each). The
+// barrier sits between the halves: every wave has then read both halves of step ks, whose
+// stage takes the loads of step ks + kStages, in the second half of this step and the first
+// of the next; and each has seen its own loads of step ks + 1 land.
 constexpr int kWaves = 4;
-constexpr int kStages = 3;
 constexpr int kBand = 8;  // M tiles per traversal band
+constexpr int kCus = 256, kEdge = 256;
 
 template <int FM, int FN>
 struct Shape {
+  static constexpr int kStages = FM * FN == 16 ? 3 : 4;
   static constexpr int TM = 64 * FM, TN = 64 * FN;
   static constexpr int CodesA = TM * 64, CodesW = TN * 64;
   static constexpr int ScaleA = TM / 128 * 512, ScaleW = TN / 128 * 512;
   static constexpr int Stage = CodesA + CodesW + ScaleA + ScaleW;
   static constexpr int LoadsA = CodesA / 1024 / kWaves, LoadsW = CodesW / 1024 / kWaves;
-  static constexpr int LoadsS = (ScaleA + ScaleW) / 256 / kWaves;  // a dword a lane
+  static constexpr int Pieces = (ScaleA + ScaleW) / 256;            // scale loads: a dword a lane
+  static constexpr int LoadsS = (Pieces + kWaves - 1) / kWaves;
   static constexpr int Loads = LoadsA + LoadsW + LoadsS;
   static constexpr int RowBytes = 32 * FN * 2 + 16;                 // epilogue staging, padded
   static constexpr int Staging = kWaves * 32 * RowBytes;
   static constexpr int Lds = kStages * Stage > Staging ? kStages * Stage : Staging;
   static_assert(CodesA % (1024 * kWaves) == 0 && CodesW % (1024 * kWaves) == 0, "even code loads");
-  static_assert((ScaleA + ScaleW) % (256 * kWaves) == 0, "even scale loads");
   static_assert((kStages - 2) * Loads < 64, "vmcnt immediate");
+  static_assert((FM == 4 || FM == 2) && (FN == 4 || FN == 2), "scale reads");
 };
 
 // where 16-byte chunk c of row r lies in the row's 64 LDS bytes: fragment reads (32 rows,
@@ -85,25 +90,15 @@ __device__ __forceinline__ void wait_loads() {
   __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));
 }
 
+// the tile at rows m0, columns n0
 template <int FM, int FN>
-__global__ __launch_bounds__(64 * kWaves, 1) void mx_gemm_kernel(MxGemmArgs a) {
+__device__ __forceinline__ void run_tile(const MxGemmArgs& a, int64_t m0, int64_t n0, uint8_t* smem) {
   using T = Shape<FM, FN>;
-  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int kStages = T::kStages;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1;
   const int lr = lane & 31, h = lane >> 5;
-
-  // Workgroups go round-robin to the 8 XCDs: each XCD gets one contiguous range of tiles,
-  // numbered in bands of kBand M tiles, so that its L2 keeps the band's rows of A.
-  const int total = a.tiles_m * a.tiles_n;
-  const int per = total / 8, rem = total % 8, x = blockIdx.x & 7;
-  const int tile = x * per + (x < rem ? x : rem) + (blockIdx.x >> 3);
-  const int band = tile / (kBand * a.tiles_n);
-  const int inside = tile - band * kBand * a.tiles_n;
-  const int height = a.tiles_m - band * kBand < kBand ? a.tiles_m - band * kBand : kBand;
-  const int64_t m0 = (int64_t)(band * kBand + inside % height) * T::TM;
-  const int64_t n0 = (int64_t)(inside / height) * T::TN;
 
   // Buffers of the tile's own rows: reads past them return zero (codes 0 under scale 0).
   const int krow = (int)(a.k >> 1);
@@ -134,7 +129,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void mx_gemm_kernel(MxGemmArgs a) {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(is_a ? rA : rW, (lds_ptr_t*)(st + (is_a ? 0 : T::CodesA) + j * 1024), 16,
                                                off, 0, 0, 0);
     } else {
-      const int q = wave * T::LoadsS + (idx - T::LoadsA - T::LoadsW);  // 256-byte piece of the scales
+      const int q = (wave * T::LoadsS + (idx - T::LoadsA - T::LoadsW)) % T::Pieces;  // some twice if uneven
       const bool is_a = q * 256 < T::ScaleA;
       const int rel = is_a ? q : q - T::ScaleA / 256;
       const int off = (rel >> 1) * srow + ks * 512 + (rel & 1) * 256 + lane * 4;
@@ -142,36 +137,36 @@ __global__ __launch_bounds__(64 * kWaves, 1) void mx_gemm_kernel(MxGemmArgs a) {
                                                off, 0, 0, 0);
     }
   };
-  // half kk: lane half h takes block (chunk) 2 kk + h of the step
-  auto read_codes = [&](int stage, int kk, u32x4_t (&ca)[FM], u32x4_t (&cw)[FN]) __attribute__((always_inline)) {
+  // half kk: lane half h takes block (chunk) 2 kk + h of the step; fragment f of A, then W
+  auto read_code = [&](int stage, int kk, int f, u32x4_t (&ca)[FM], u32x4_t (&cw)[FN]) __attribute__((always_inline)) {
     const uint8_t* st = smem + stage * T::Stage;
     const int c = 2 * kk + h;
-#pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const int r = (wm * FM + i) * 32 + lr;
-      ca[i] = *(const u32x4_t*)(st + r * 64 + chunk_at(r, c) * 16);
-    }
-#pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      const int r = (wn * FN + j) * 32 + lr;
-      cw[j] = *(const u32x4_t*)(st + T::CodesA + r * 64 + chunk_at(r, c) * 16);
+    if (f < FM) {
+      const int r = (wm * FM + f) * 32 + lr;
+      ca[f] = *(const u32x4_t*)(st + r * 64 + chunk_at(r, c) * 16);
+    } else {
+      const int r = (wn * FN + f - FM) * 32 + lr;
+      cw[f - FM] = *(const u32x4_t*)(st + T::CodesA + r * 64 + chunk_at(r, c) * 16);
     }
   };
-  // the four scale bytes of each row, moved so that bytes 0 and 2 are the lane half's
-  auto read_scales = [&](int stage, uint32_t (&sa)[FM], uint32_t (&sw)[FN]) __attribute__((always_inline)) {
-    const uint8_t* ss = smem + stage * T::Stage + T::CodesA + T::CodesW;
+  // the four scale bytes of the rows of a side's fragments: 32-row groups lie next to each
+  // other, so a lane's are one run
+  auto read_scales = [&](int stage, bool is_a, uint32_t (&sc)[FM + FN]) __attribute__((always_inline)) {
+    const int g = is_a ? wm * FM : wn * FN, n = is_a ? FM : FN, at = is_a ? 0 : FM;
+    const uint8_t* p = smem + stage * T::Stage + T::CodesA + T::CodesW + (is_a ? 0 : T::ScaleA) + (g >> 2) * 512 +
+                       lr * 16 + (g & 3) * 4;
+    if (n == 4) {
+      const u32x4_t v = *(const u32x4_t*)p;
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const int f = wm * FM + i;  // 32-row group of the tile
-      sa[i] = *(const uint32_t*)(ss + (f >> 2) * 512 + lr * 16 + (f & 3) * 4);
-    }
-#pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      const int f = wn * FN + j;
-      sw[j] = *(const uint32_t*)(ss + T::ScaleA + (f >> 2) * 512 + lr * 16 + (f & 3) * 4);
+      for (int i = 0; i < 4; ++i) sc[(at + i) % (FM + FN)] = v[i];
+    } else {
+      const u32x2_t v = *(const u32x2_t*)p;
+      sc[at] = v[0];
+      sc[at + 1] = v[1];
     }
   };
 
+  constexpr int kEarly = T::Loads / 2;  // loads of a step in its first part
   f32x16_t acc[FN][FM];
 #pragma unroll
   for (int j = 0; j < FN; ++j)
@@ -183,52 +178,63 @@ __global__ __launch_bounds__(64 * kWaves, 1) void mx_gemm_kernel(MxGemmArgs a) {
 #pragma unroll
   for (int s = 0; s < kStages; ++s)
 #pragma unroll
-    for (int idx = 0; idx < T::Loads; ++idx) issue(s, s, idx);
-  wait_loads<(kStages - 1) * T::Loads>();
+    for (int idx = 0; idx < (s + 1 < kStages ? T::Loads : kEarly); ++idx) issue(s, s, idx);
+  wait_loads<(kStages - 2) * T::Loads + kEarly>();
   barrier();
 
   u32x4_t ca[2][FM], cw[2][FN];
-  uint32_t sa[2][FM], sw[2][FN];
-  read_scales(0, sa[0], sw[0]);
-  read_codes(0, 0, ca[0], cw[0]);
+  uint32_t sc[FM + FN];
+#pragma unroll
+  for (int f = 0; f < FM + FN; ++f) read_code(0, 0, f, ca[0], cw[0]);
+  read_scales(0, true, sc);
+  read_scales(0, false, sc);
 
-  auto kstep = [&](int ks, int stage, int set) __attribute__((always_inline)) {
-    const int next = stage + 1 == kStages ? 0 : stage + 1;
-    read_codes(stage, 1, ca[1], cw[1]);
-    uint32_t ha[FM], hw[FN];
+  constexpr int P = FM * FN, F = FM + FN;
+  auto kstep = [&](int ks, int stage) __attribute__((always_inline)) {
+    const int next = stage + 1 == kStages ? 0 : stage + 1, last = stage == 0 ? kStages - 1 : stage - 1;
+    uint32_t hs[F];  // bytes 0 and 2: the lane half's blocks of the two halves
 #pragma unroll
-    for (int i = 0; i < FM; ++i) ha[i] = sa[set][i] >> (8 * h);
+    for (int f = 0; f < F; ++f) hs[f] = sc[f] >> (8 * h);
 #pragma unroll
-    for (int j = 0; j < FN; ++j) hw[j] = sw[set][j] >> (8 * h);
+    for (int p = 0; p < P; ++p) {
+      const int j = p / FM, i = p % FM;
+      acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fp4_operand(cw[0][j]), fp4_operand(ca[0][i]),
+                                                                  acc[j][i], 4, 4, 0, (int)hs[FM + j], 0, (int)hs[i]);
+      __builtin_amdgcn_sched_barrier(0);  // its wait for operands comes before the reads below
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
+      for (int f = 0; f < F; ++f)
+        if (f * (P / 2) / F == p) read_code(stage, 1, f, ca[1], cw[1]);
 #pragma unroll
-      for (int i = 0; i < FM; ++i)
-        acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fp4_operand(cw[0][j]), fp4_operand(ca[0][i]),
-                                                                    acc[j][i], 4, 4, 0, (int)hw[j], 0, (int)ha[i]);
-    asm volatile("" ::: "memory");
+      for (int idx = kEarly; idx < T::Loads; ++idx)
+        if ((idx - kEarly) * P / (T::Loads - kEarly) == p) issue(ks - 1 + kStages, last, idx);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this stage's reads are done
     wait_loads<(kStages - 2) * T::Loads>();
     barrier();
 #pragma unroll
-    for (int idx = 0; idx < T::Loads; ++idx) issue(ks + kStages, stage, idx);
-    read_scales(next, sa[set ^ 1], sw[set ^ 1]);
-    read_codes(next, 0, ca[0], cw[0]);
+    for (int p = 0; p < P; ++p) {
+      const int j = p / FM, i = p % FM;
+      acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fp4_operand(cw[1][j]), fp4_operand(ca[1][i]),
+                                                                  acc[j][i], 4, 4, 2, (int)hs[FM + j], 2, (int)hs[i]);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
+      for (int f = 0; f < F + 2; ++f) {
+        if (f * (P * 3 / 4) / (F + 2) != p) continue;
+        if (f < F) read_code(next, 0, f, ca[0], cw[0]);
+        else read_scales(next, f == F, sc);
+      }
 #pragma unroll
-      for (int i = 0; i < FM; ++i)
-        acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fp4_operand(cw[1][j]), fp4_operand(ca[1][i]),
-                                                                    acc[j][i], 4, 4, 2, (int)hw[j], 2, (int)ha[i]);
+      for (int idx = 0; idx < kEarly; ++idx)
+        if (idx * P / kEarly == p) issue(ks + kStages, stage, idx);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
   int stage = 0, ks = 0;
-  for (; ks + 1 < a.groups; ks += 2) {
-    kstep(ks, stage, 0);
-    stage = stage + 1 == kStages ? 0 : stage + 1;
-    kstep(ks + 1, stage, 1);
+  for (; ks < a.groups; ++ks) {
+    kstep(ks, stage);
     stage = stage + 1 == kStages ? 0 : stage + 1;
   }
-  if (ks < a.groups) kstep(ks, stage, 0);
 
   // ---- epilogue: 32 rows at a time through the wave's part of LDS, so that a store writes
   // whole row pieces. The loads past the last step are still writing zeros: wait first. ----
@@ -268,6 +274,37 @@ __global__ __launch_bounds__(64 * kWaves, 1) void mx_gemm_kernel(MxGemmArgs a) {
     __builtin_amdgcn_s_waitcnt(0xC07F);
     asm volatile("" ::: "memory");
   }
+}
+
+// Workgroups go round-robin to the 8 XCDs: each XCD gets one contiguous range of the whole
+// tiles, numbered in bands of kBand M tiles, so that its L2 keeps the band's rows of A. The
+// tiles of a last round that would leave half of the CUs idle or more are run as two or four
+// parts each, a workgroup a part.
+__global__ __launch_bounds__(64 * kWaves, 1) void mx_gemm_kernel(MxGemmArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int b = blockIdx.x;
+  int tile, part = 0;
+  if (b < a.whole) {
+    const int per = a.whole / 8, rem = a.whole % 8, x = b & 7;
+    tile = x * per + (x < rem ? x : rem) + (b >> 3);
+  } else {
+    tile = a.whole + (b - a.whole) / a.parts;
+    part = (b - a.whole) % a.parts;
+  }
+  const int band = tile / (kBand * a.tiles_n);
+  const int inside = tile - band * kBand * a.tiles_n;
+  const int height = a.tiles_m - band * kBand < kBand ? a.tiles_m - band * kBand : kBand;
+  int64_t m0 = (int64_t)(band * kBand + inside % height) * kEdge;
+  int64_t n0 = (int64_t)(inside / height) * kEdge;
+  if (b < a.whole) {
+    run_tile<4, 4>(a, m0, n0, smem);
+    return;
+  }
+  m0 += (part & 1) * (kEdge / 2);
+  n0 += (part >> 1) * (kEdge / 2);
+  if (m0 >= a.m || n0 >= a.n) return;
+  if (a.parts == 2) run_tile<2, 4>(a, m0, n0, smem);
+  else run_tile<2, 2>(a, m0, n0, smem);
 }
 
 // ---- few rows ------------------------------------------------------------------------------
@@ -348,12 +385,20 @@ __global__ __launch_bounds__(64 * kThinWaves, 2) void mx_gemm_thin_kernel(MxGemm
   }
 }
 
-template <int FM, int FN>
+constexpr int kLds = Shape<4, 4>::Lds;
+static_assert(Shape<2, 4>::Lds <= kLds && Shape<2, 2>::Lds <= kLds, "LDS");
+
+// Whole rounds of 256 x 256 tiles, which need the fewest operand bytes a product; in a last
+// round (or the only one) that fills at most half of the CUs, 128 x 256 halves, and 128 x 128
+// quarters where even those fill at most half. Measured at K 7168: a round of whole tiles
+// takes 50 us, of halves 32, of quarters 21.
 hipError_t launch_tiles(MxGemmArgs a, hipStream_t stream) {
-  using T = Shape<FM, FN>;
-  a.tiles_m = (int)((a.m + T::TM - 1) / T::TM);
-  a.tiles_n = (int)((a.n + T::TN - 1) / T::TN);
-  mx_gemm_kernel<FM, FN><<<a.tiles_m * a.tiles_n, 64 * kWaves, T::Lds, stream>>>(a);
+  a.tiles_m = (int)((a.m + kEdge - 1) / kEdge);
+  a.tiles_n = (int)((a.n + kEdge - 1) / kEdge);
+  const int total = a.tiles_m * a.tiles_n, last = total % kCus;
+  a.parts = last * 4 <= kCus ? 4 : last * 2 <= kCus ? 2 : 1;
+  a.whole = a.parts == 1 ? total : total - last;
+  mx_gemm_kernel<<<a.whole + (total - a.whole) * a.parts, 64 * kWaves, kLds, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -366,26 +411,17 @@ hipError_t launch_thin(const MxGemmArgs& a, hipStream_t stream) {
 }  // namespace
 
 hipError_t mx_gemm_setup() {
-  hipError_t e = hipFuncSetAttribute((const void*)mx_gemm_kernel<4, 4>, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                     Shape<4, 4>::Lds);
-  if (e == hipSuccess)
-    e = hipFuncSetAttribute((const void*)mx_gemm_kernel<2, 2>, hipFuncAttributeMaxDynamicSharedMemorySize,
-                            Shape<2, 2>::Lds);
-  return e;
+  return hipFuncSetAttribute((const void*)mx_gemm_kernel, hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
 }
 
 hipError_t launch_mx_gemm(const uint8_t* aq, const uint8_t* as, const uint8_t* wq, const uint8_t* ws, uint16_t* d,
                           int64_t ldd, int64_t m, int64_t n, int64_t k, hipStream_t stream) {
-  MxGemmArgs a{aq, as, wq, ws, d, ldd, m, n, k, (int)((k / kMxBlock + 3) / 4), 0, 0,
+  MxGemmArgs a{aq, as, wq, ws, d, ldd, m, n, k, (int)((k / kMxBlock + 3) / 4), 0, 0, 0, 1,
                n % 8 == 0 && ldd % 8 == 0 && ((uintptr_t)d & 15u) == 0};
   if (m <= 16) return launch_thin<1, 1>(a, stream);
   if (m <= 32) return launch_thin<2, 1>(a, stream);
   if (m <= 64) return launch_thin<4, 1>(a, stream);
-  // whole 256 x 256 tiles need the fewest operand bytes per product; with too few of them
-  // to give every CU one, quarters
-  const int64_t big = ((m + 255) / 256) * ((n + 255) / 256);
-  if (big < 256) return launch_tiles<2, 2>(a, stream);
-  return launch_tiles<4, 4>(a, stream);
+  return launch_tiles(a, stream);
 }
 
 }  // namespace nvfp4
