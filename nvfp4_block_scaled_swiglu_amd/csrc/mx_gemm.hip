@@ -309,15 +309,15 @@ __global__ __launch_bounds__(64 * kWaves, 1) void mx_gemm_kernel(MxGemmArgs a) {
 
 // ---- few rows ------------------------------------------------------------------------------
 // Up to 64 rows of A: the weight is read once and that is all there is to it. A workgroup
-// takes 16 NT columns and its waves split K, so that n / (16 NT) workgroups of 8 waves keep
-// enough loads in flight; operands go from memory to registers (16x16x128: lane (r, u) has
-// row r, block u of the step). The waves' sums are joined in LDS in wave order.
-constexpr int kThinWaves = 8;
-constexpr int kThinSteps = 4;  // K steps of 128 in flight per wave
-
-template <int MT, int NT>
-__global__ __launch_bounds__(64 * kThinWaves, 2) void mx_gemm_thin_kernel(MxGemmArgs a) {
-  __shared__ float red[kThinWaves * MT * NT * 256];
+// takes 16 NT columns and its W waves split K; operands go from memory to registers
+// (16x16x128: lane (r, u) has row r, block u of the step), a step ahead of their product. The
+// waves' sums are joined in LDS in wave order. Every workgroup reads all of A, from L2: what
+// A's registers cost beside the weight's decides NT (launch_mx_gemm).
+// Measured, in a graph: 1 x 5376 x 14336 14.3 us (2.9 TB/s of weight, 2.7 us of it per
+// launch). More steps ahead, or more waves, change nothing.
+template <int MT, int NT, int W>
+__global__ __launch_bounds__(64 * W, 2) void mx_gemm_thin_kernel(MxGemmArgs a) {
+  __shared__ float red[W * MT * NT * 256];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, u = lane >> 4;
@@ -338,35 +338,49 @@ __global__ __launch_bounds__(64 * kThinWaves, 2) void mx_gemm_thin_kernel(MxGemm
 #pragma unroll
     for (int i = 0; i < MT; ++i) acc[j][i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-  for (int k0 = wave * kThinSteps; k0 < a.groups; k0 += kThinWaves * kThinSteps) {
-    u32x4_t cw[kThinSteps][NT], ca[kThinSteps][MT];
-    uint32_t sw[kThinSteps][NT], sa[kThinSteps][MT];
+  // the waves share the K steps evenly, each a run of them
+  struct Step {
+    u32x4_t cw[NT], ca[MT];
+    uint32_t sw[NT], sa[MT];
+  };
+  const int k_end = a.groups * (wave + 1) / W;
+  auto load = [&](Step& x, int ks) __attribute__((always_inline)) {
+    const int kb = ks * 64 + u * 16;
+    const bool in = (kb < krow) & (ks < k_end);  // past K or the wave's run: codes 0, scales 0
 #pragma unroll
-    for (int s = 0; s < kThinSteps; ++s) {
-      const int kb = (k0 + s) * 64 + u * 16;
-      const bool in = kb < krow;  // past K: codes 0
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int row = j * 16 + r;
-        cw[s][j] = __builtin_amdgcn_raw_buffer_load_b128(rW, in ? row * krow + kb : 0x7FFFFFF0, 0, 0);
-        sw[s][j] = __builtin_amdgcn_raw_buffer_load_b32(rSW, in ? (k0 + s) * 512 + scale_at(nrow + row) : 0x7FFFFFF0, 0, 0);
-      }
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const int row = i * 16 + r;
-        ca[s][i] = __builtin_amdgcn_raw_buffer_load_b128(rA, in ? row * krow + kb : 0x7FFFFFF0, 0, 0);
-        sa[s][i] = __builtin_amdgcn_raw_buffer_load_b32(rSA, in ? (k0 + s) * 512 + scale_at(row) : 0x7FFFFFF0, 0, 0);
-      }
+    for (int j = 0; j < NT; ++j) {
+      const int row = j * 16 + r;
+      x.cw[j] = __builtin_amdgcn_raw_buffer_load_b128(rW, in ? row * krow + kb : 0x7FFFFFF0, 0, 0);
+      x.sw[j] = __builtin_amdgcn_raw_buffer_load_b32(rSW, in ? ks * 512 + scale_at(nrow + row) : 0x7FFFFFF0, 0, 0);
     }
 #pragma unroll
-    for (int s = 0; s < kThinSteps; ++s)
+    for (int i = 0; i < MT; ++i) {
+      const int row = i * 16 + r;
+      x.ca[i] = __builtin_amdgcn_raw_buffer_load_b128(rA, in ? row * krow + kb : 0x7FFFFFF0, 0, 0);
+      x.sa[i] = __builtin_amdgcn_raw_buffer_load_b32(rSA, in ? ks * 512 + scale_at(row) : 0x7FFFFFF0, 0, 0);
+    }
+  };
+  auto multiply = [&](const Step& x) __attribute__((always_inline)) {
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-          acc[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              fp4_operand(cw[s][j]), fp4_operand(ca[s][i]), acc[j][i], 4, 4, 0, (int)(sw[s][j] >> (8 * u)), 0,
-              (int)(sa[s][i] >> (8 * u)));
+      for (int i = 0; i < MT; ++i)
+        acc[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fp4_operand(x.cw[j]), fp4_operand(x.ca[i]), acc[j][i],
+                                                                     4, 4, 0, (int)(x.sw[j] >> (8 * u)), 0,
+                                                                     (int)(x.sa[i] >> (8 * u)));
+  };
+  Step x, y;
+  int ks = a.groups * wave / W;
+  load(x, ks);
+  for (; ks < k_end; ks += 2) {
+    load(y, ks + 1);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(x);
+    __builtin_amdgcn_sched_barrier(0);
+    load(x, ks + 2);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(y);
+    __builtin_amdgcn_sched_barrier(0);
   }
   // lane (r, u) holds row m = r, columns 4u .. 4u + 3 of each 16 x 16 tile
 #pragma unroll
@@ -374,13 +388,13 @@ __global__ __launch_bounds__(64 * kThinWaves, 2) void mx_gemm_thin_kernel(MxGemm
 #pragma unroll
     for (int i = 0; i < MT; ++i) *(f32x4_t*)(red + ((wave * NT + j) * MT + i) * 256 + lane * 4) = acc[j][i];
   __syncthreads();
-  for (int e = threadIdx.x; e < MT * NT * 256; e += 64 * kThinWaves) {
+  for (int e = threadIdx.x; e < MT * NT * 256; e += 64 * W) {
     // e: column within the workgroup's fastest, then row, so that stores run along D's rows
     const int col = e % (16 * NT), row = e / (16 * NT);
     const int at = ((col >> 4) * MT + (row >> 4)) * 256 + (((col & 15) >> 2) * 16 + (row & 15)) * 4 + (col & 3);
     float y = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kThinWaves; ++w) y += red[w * MT * NT * 256 + at];
+    for (int w = 0; w < W; ++w) y += red[w * MT * NT * 256 + at];
     if (row < a.m && n0 + col < a.n) a.d[row * a.ldd + n0 + col] = (uint16_t)pack_bf16(y, 0.0f);
   }
 }
@@ -403,9 +417,25 @@ hipError_t launch_tiles(MxGemmArgs a, hipStream_t stream) {
 }
 
 template <int MT, int NT>
-hipError_t launch_thin(const MxGemmArgs& a, hipStream_t stream) {
-  mx_gemm_thin_kernel<MT, NT><<<(unsigned)((a.n + 16 * NT - 1) / (16 * NT)), 64 * kThinWaves, 0, stream>>>(a);
+hipError_t launch_thin_columns(const MxGemmArgs& a, hipStream_t stream) {
+  constexpr int W = MT == 4 ? 4 : 8;
+  mx_gemm_thin_kernel<MT, NT, W><<<(unsigned)((a.n + 16 * NT - 1) / (16 * NT)), 64 * W, 0, stream>>>(a);
   return hipGetLastError();
+}
+
+// As many columns a workgroup as still leave 160 workgroups (5 in 8 CUs): A is read once for
+// each workgroup, so more columns save its bytes, but idle CUs cost more than they save.
+// Measured for 1, 2 and 4 tiles: 1 x 5376 x 14336 17.5, 14.3, 23.3 us; 32 x 28672 x 5376 46,
+// 33, 27 us; 64 x 5376 x 7168 26, 17.3, 23.5 us.
+constexpr int64_t kThinGroups = 160;
+
+template <int MT>
+hipError_t launch_thin(const MxGemmArgs& a, hipStream_t stream) {
+  if constexpr (MT < 4) {
+    if (a.n >= kThinGroups * 64) return launch_thin_columns<MT, 4>(a, stream);
+  }
+  if (a.n >= kThinGroups * 32) return launch_thin_columns<MT, 2>(a, stream);
+  return launch_thin_columns<MT, 1>(a, stream);
 }
 
 }  // namespace
@@ -418,9 +448,12 @@ hipError_t launch_mx_gemm(const uint8_t* aq, const uint8_t* as, const uint8_t* w
                           int64_t ldd, int64_t m, int64_t n, int64_t k, hipStream_t stream) {
   MxGemmArgs a{aq, as, wq, ws, d, ldd, m, n, k, (int)((k / kMxBlock + 3) / 4), 0, 0, 0, 1,
                n % 8 == 0 && ldd % 8 == 0 && ((uintptr_t)d & 15u) == 0};
-  if (m <= 16) return launch_thin<1, 1>(a, stream);
-  if (m <= 32) return launch_thin<2, 1>(a, stream);
-  if (m <= 64) return launch_thin<4, 1>(a, stream);
+  // The thin form up to 32 rows, and up to 64 where a wide weight does not give the tiles
+  // enough workgroups: 48 x 5376 x 7168 15.9 us, as tiles 18.2; 48 x 16128 x 5376 18.5 us, as
+  // tiles 15.8; 32 x 5376 x 14336 21.9 us, as tiles 32.1.
+  if (m <= 16) return launch_thin<1>(a, stream);
+  if (m <= 32) return launch_thin<2>(a, stream);
+  if (m <= 64 && n < kThinGroups * 64) return launch_thin<4>(a, stream);
   return launch_tiles(a, stream);
 }
 

@@ -118,7 +118,7 @@ class Mxfp4Cache:
 def empty_mxfp4(rows: int, k: int, device) -> Mxfp4Tensor:
     import torch
     return Mxfp4Tensor(qdata=torch.empty((rows, k // 2), dtype=torch.uint8, device=device),
-                       scales=torch.empty((max(0, mxfp4_scale_bytes(rows, k)),), dtype=torch.uint8, device=device),
+                       scales=torch.empty((max(0, _scale_bytes(rows, k)),), dtype=torch.uint8, device=device),
                        rows=rows, k=k)
 
 
@@ -155,9 +155,13 @@ def _buffer(t, name: str, size: int):
 def _packed(t, name: str):
     if not isinstance(t, Mxfp4Tensor):
         raise ValueError(f"{name} must be an Mxfp4Tensor")
-    _buffer(t.qdata, f"{name}.qdata", mxfp4_qdata_bytes(t.rows, t.k))
-    _buffer(t.scales, f"{name}.scales", mxfp4_scale_bytes(t.rows, t.k))
+    _buffer(t.qdata, name, t.rows * (t.k // 2))
+    _buffer(t.scales, name, _scale_bytes(t.rows, t.k))
     return t
+
+
+def _scale_bytes(rows: int, k: int) -> int:  # mxfp4_scale_bytes without the call
+    return -(-rows // 128) * 128 * (-(-(k // 32) // 4) * 4)
 
 
 def _int32(t, name: str, dim: int):
@@ -183,37 +187,51 @@ def _strides(t) -> Tuple[int, int]:
     return (t.stride(0), dim if heads <= 1 else t.stride(1))
 
 
+def _current_stream(index: int) -> int:
+    """The handle of a device's current stream, without the object around it where torch has it so."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else int(torch.cuda.current_stream(index).cuda_stream)
+
+
 class _On:
     """The device and stream of a call: enter it to allocate outputs and to launch."""
 
+    __slots__ = ("device", "handle", "stack")
+
     def __init__(self, stream, *tensors):
         import torch
+        index = tensors[0].get_device()
+        for t in tensors:
+            if t.get_device() != index:
+                raise ValueError("all tensors of a call must be on one device")
         self.device = tensors[0].device
-        if any(t.device != self.device for t in tensors):
-            raise ValueError("all tensors of a call must be on one device")
+        self.stack = None
+        if stream is None and index == torch.cuda.current_device():  # nothing to switch
+            self.handle = _current_stream(index)
+            return
         self.stack = contextlib.ExitStack()
-        self.other = None
-        if self.device.index != torch.cuda.current_device():
-            self.stack.enter_context(torch.cuda.device(self.device))
         try:
+            self.stack.enter_context(torch.cuda.device(self.device))
             current = torch.cuda.current_stream()
             if stream is not None and stream != current:
                 if getattr(stream, "device", self.device) != self.device:
                     raise ValueError("stream is of another device than the tensors")
-                self.other = stream
                 self.stack.enter_context(torch.cuda.stream(stream))
                 for t in tensors:
                     t.record_stream(stream)
+                current = stream
+            self.handle = int(current.cuda_stream)
         except BaseException:
             self.stack.close()
             raise
-        self.handle = int((current if self.other is None else stream).cuda_stream)
 
     def __enter__(self):
         return self
 
     def __exit__(self, *exc):
-        return self.stack.__exit__(*exc)
+        if self.stack is not None:
+            return self.stack.__exit__(*exc)
 
 
 # ---- quantization --------------------------------------------------------------------------
@@ -295,17 +313,20 @@ def mxfp4_gemm_bf16out(a: Mxfp4Tensor, w: Mxfp4Tensor, out=None, stream=None, st
 
 def _cache(c: Mxfp4Cache):
     """The cache's C form and its tensors."""
+    import torch
     if not isinstance(c, Mxfp4Cache):
         raise ValueError("cache must be an Mxfp4Cache")
-    tensors = (c.k_codes, c.k_scales, c.v_codes, c.v_scales)
-    for t, name in zip(tensors, ("k_codes", "k_scales", "v_codes", "v_scales")):
-        _buffer(t, f"cache.{name}", 0)
-    if c.k_codes.dim() != 4:
+    kc, ks, vc, vs = tensors = (c.k_codes, c.k_scales, c.v_codes, c.v_scales)
+    for t in tensors:
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8 or not t.is_cuda or not t.is_contiguous():
+            raise ValueError("the cache's tensors must be contiguous uint8 CUDA tensors")
+    if kc.dim() != 4:
         raise ValueError("cache.k_codes must be [num_pages, kv_heads, page_size, head_dim / 2]")
-    pages, heads, size, half = c.k_codes.shape
-    if any(tuple(t.shape) != (pages, heads, size, n) for t, n in zip(tensors, (half, half // 16, half, half // 16))):
+    pages, heads, size, half = kc.shape
+    scales = (pages, heads, size, half // 16)
+    if vc.shape != kc.shape or ks.shape != scales or vs.shape != scales:
         raise ValueError("the cache's codes and scales disagree in shape")
-    return _CCache(*(t.data_ptr() for t in tensors), pages, size, heads, 2 * half), tensors
+    return _CCache(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), pages, size, heads, 2 * half), tensors
 
 
 def _batch(block_table, seq_lens, cu_seqlens, tokens: int):
