@@ -39,7 +39,7 @@ struct MxAttnPlan {
 // writes and reads every row once more in fp32, so only what leaves CUs idle is split.
 inline MxAttnPlan mx_attention_plan(int64_t tokens, int64_t batch, int64_t heads, int64_t kv_heads, int64_t head_dim,
                                     int64_t max_kv, int64_t window, int64_t sinks) {
-    constexpr int64_t kMinTiles = 2;
+  constexpr int64_t kMinTiles = 2;
   MxAttnPlan p{true, 1, 1};
   if (tokens <= 0 || batch <= 0) return p;
   const int64_t group = heads / kv_heads;

@@ -2,10 +2,12 @@
 // (gfx950): prompts and prompt chunks. The operator and the packing of rows and heads are
 // those of mx_attn.hip.
 //
-// What bounds it is arithmetic: the two matrix products, and one exp2 per score beside them.
-// A workgroup has 128 RB packed rows, 32 RB to a wave, and walks the tokens 64 at a time. A
-// tile's codes are decoded once for the workgroup, into bf16 in LDS, and the products run on
-// v_mfma_f32_32x32x16_bf16 in the transposed form, lane (n, h) = (lane & 31, lane >> 5):
+// What bounds it is the issue of instructions: the two matrix products, one exp2 per score
+// and the rounding of its result, and the reads from LDS go side by side (taking any one of
+// them out gains less than a tenth). A workgroup has 256 packed rows (D = 256: 128), 32 RB to
+// a wave, and walks the tokens 64 at a time. A tile's codes are decoded once for the
+// workgroup, into bf16 in LDS, and the products run on v_mfma_f32_32x32x16_bf16 in the
+// transposed form, lane (n, h) = (lane & 31, lane >> 5):
 //
 //   S^T = K Q^T    A: token n, elements 16 s + 8 h .. + 7 of step s, a 16-byte LDS read.
 //                  S^T comes out with lane (n, h) holding packed row n and, of 32 tokens,
@@ -14,12 +16,13 @@
 //                  tokens of step s. A: element n of a block of 32, the same 8 tokens - V is
 //                  laid in LDS by element with its tokens in that order, again one read.
 //
-// Each wave reads the whole tile from LDS for its 32 RB rows; with 64 rows (RB = 2) that is
-// half of what LDS can deliver in the time of the products. O, Q, the scores of two halves,
-// the weights and the fragments read ahead are then about 400 registers: one wave a SIMD, so
-// overlap comes from the instruction stream, and every instruction counts. A tile goes in
-// two halves of 32 tokens, each in two phases of 2 D / 16 matrix instructions beside what
-// else is due:
+// Each wave reads the whole tile from LDS for its 32 RB rows. Measured, 4,096 tokens, 32 heads
+// over 8, twice, D = 64: four waves of 64 rows 205 us, two workgroups a CU; eight of 32 rows
+// 245 us. 1,500 tokens, four times, D = 128: eight waves of 32 rows, two a SIMD, 125 us; four
+// of 64 rows, one a SIMD, 151 us. D = 256 has registers for neither and takes four of 32.
+// Either way waves are few, so overlap comes from the instruction stream. A tile goes in two
+// halves of 32 tokens, each in two phases of RB D / 16 matrix instructions beside what else
+// is due:
 //
 //   1  S1 = K[t]1 Q       ||  P = exp2(S0)                  ||  read V[t]0
 //   2  O += V[t]0 P       ||  decode V[t + 1] into LDS      ||  read K[t + 1]0   | barrier
@@ -37,35 +40,36 @@
 
 #include "mx_attn.hpp"
 
-
 namespace nvfp4 {
 
 namespace {
 
-constexpr int kWaves = 4;
-constexpr int kTile = 64;  // tokens per step: 16 to a wave when they are decoded
+constexpr int kTile = 64;  // tokens per step
 
 // A raise is due when the weights of a lane's 16 tokens add up to more: some weight is then
 // above 2^8, and none that passes is above 2^12.
 constexpr float kMostSum = 4096.0f;
 
-// K rows are padded by 16 bytes; in V rows (64 tokens, 8 chunks of 16 bytes) chunk c lies at
-// v_chunk: either way the 16 rows that a read phase meets lie in different banks
-__device__ __forceinline__ int v_chunk(int d, int c) { return c ^ (((d >> 1) ^ (d >> 3)) & 7); }
+// K rows are padded by 16 bytes; in V rows (64 tokens, 128 bytes) the 16-byte pieces are
+// permuted by element. Either way the 16 rows that a phase of a 16-byte read meets lie in
+// different banks (16 in order, or the rows whose bits 2, 3 and 4 have an even sum), and of V
+// so do those that 32 lanes write, 4 or 16 elements apart.
+__device__ __forceinline__ int v_chunk(int e, int c) { return c ^ (((e >> 1) ^ (e >> 4) ^ (e >> 7)) & 7); }
 
 template <int D>
 struct Lds {
   static constexpr int KRow = D * 2 + 16;
   static constexpr int K = kTile * KRow, V = D * kTile * 2;   // bytes of a tile
   static constexpr int Nan = D / 32 * kTile;                  // V bytes that are NaN, [block][token]
-  static constexpr int VAt = 2 * K, NanAt = VAt + 2 * V, FlagAt = NanAt + 2 * Nan, Bytes = FlagAt + 2 * 4 * kWaves;
+  static constexpr int VAt = 2 * K, NanAt = VAt + 2 * V, FlagAt = NanAt + 2 * Nan, Bytes = FlagAt + 2 * 4 * 8;
   static_assert(Bytes <= 160 * 1024, "LDS");
 };
 
-template <int D, int RB>
-__global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : 1) void mx_attention_prompt_kernel(MxAttnArgs a) {
+template <int D, int RB, int kWaves>
+__global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : kWaves / 4) void mx_attention_prompt_kernel(MxAttnArgs a) {
   using L = Lds<D>;
   constexpr int KS = D / 16, DB = D / 32;
+  constexpr int H = kWaves / 4;  // waves that share 16 tokens of a tile, each a part of the elements
   constexpr int kRows = 32 * RB * kWaves;
   extern __shared__ __align__(16) uint8_t smem[];
 
@@ -108,15 +112,17 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : 1) void mx_attention_pro
     low[r] = mx_low(a, rows.back + i);
   }
 
-  // ---- a tile's way into LDS: wave w brings tokens 16 w .. 16 w + 15 ----
-  // K: a lane takes a quarter of a token's codes; V: D / 16 elements of four tokens
-  const int kt = lane >> 2, kq = lane & 3;          // K: token of the 16, quarter
-  const int vc = lane & 15, vq = lane >> 4;         // V: elements [vc D/16, + D/16), tokens 4 vq .. + 3
-  const int vblk = vc * (D / 16) / 32;
+  // ---- a tile's way into LDS: wave w brings tokens 16 (w % 4) .. + 15, part w / 4 of H ----
+  // K: four lanes to a token, D / 4 / H elements each; V: D / 16 / H elements of four tokens
+  constexpr int KE = D / 4 / H, VE = D / 16 / H;  // elements of a lane
+  const int grp = wave & 3, part = wave >> 2;
+  const int kt = lane >> 2, k0 = (part * 4 + (lane & 3)) * KE;
+  const int vq = (lane >> 4 & 1) * 2 + (lane >> 5), v0 = (part * 16 + (lane & 15)) * VE;
+  const int vblk = v0 / 32;
   struct Raw {
-    Words<D / 32> k;
-    uint32_t ks[D == 256 ? 2 : 1];
-    uint32_t v[4][D == 256 ? 2 : 1];
+    Words<(KE >= 8 ? KE / 8 : 1)> k;
+    uint32_t ks[KE > 32 ? 2 : 1];
+    uint32_t v[4][VE > 8 ? 2 : 1];
     uint32_t vs[4];
   };
   // The block table, 64 entries at a time, one a lane. Of a tile: the cache row of the wave's
@@ -145,63 +151,66 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : 1) void mx_attention_pro
       for (int w = 0; w < 4; ++w)
         if (__builtin_amdgcn_readlane(entry, ((t + 16 * w) >> a.b.page_shift) - base) < 0) x.there &= ~(1u << w);
     }
-    x.row = mx_cache_row(a, __builtin_amdgcn_readlane(entry, ((t + 16 * wave) >> a.b.page_shift) - base), kvh,
-                         t + 16 * wave);
+    x.row = mx_cache_row(a, __builtin_amdgcn_readlane(entry, ((t + 16 * grp) >> a.b.page_shift) - base), kvh,
+                         t + 16 * grp);
     return x;
   };
   auto load_k = [&](Raw& x, const Pages& pg) __attribute__((always_inline)) {
-    x.k = load_words<D / 32>(a.c.k_codes + pg.row * (D / 2) + (kt * (D / 2) + kq * (D / 8)));
-    const uint8_t* s = a.c.k_scales + pg.row * (D / 32) + (kt * (D / 32) + kq * (D / 4) / 32);
+    x.k = load_words<(KE >= 8 ? KE / 8 : 1)>(a.c.k_codes + pg.row * (D / 2) + (kt * (D / 2) + k0 / 2));
+    const uint8_t* s = a.c.k_scales + pg.row * (D / 32) + (kt * (D / 32) + k0 / 32);
 #pragma unroll
-    for (int b = 0; b < (D == 256 ? 2 : 1); ++b) x.ks[b] = s[b];
+    for (int b = 0; b < (KE > 32 ? 2 : 1); ++b) x.ks[b] = s[b];
   };
   auto load_v = [&](Raw& x, const Pages& pg) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint8_t* p = a.c.v_codes + pg.row * (D / 2) + ((4 * vq + i) * (D / 2) + vc * (D / 32));
-      if constexpr (D == 64) x.v[i][0] = *(const uint16_t*)p;
+      const uint8_t* p = a.c.v_codes + pg.row * (D / 2) + ((4 * vq + i) * (D / 2) + v0 / 2);
+      if constexpr (VE == 2) x.v[i][0] = *p;
+      else if constexpr (VE == 4) x.v[i][0] = *(const uint16_t*)p;
       else {
-        const Words<D / 128> w = load_words<D / 128>(p);
+        const Words<VE / 8> w = load_words<VE / 8>(p);
 #pragma unroll
-        for (int j = 0; j < D / 128; ++j) x.v[i][j] = w.w[j];
+        for (int j = 0; j < VE / 8; ++j) x.v[i][j] = w.w[j];
       }
       x.vs[i] = (a.c.v_scales + pg.row * (D / 32))[(4 * vq + i) * (D / 32) + vblk];
     }
   };
-  auto store_k = [&](const Raw& x, int buf, int e) __attribute__((always_inline)) {  // piece e of D / 32
-    uint8_t* dst = smem + buf * L::K + (wave * 16 + kt) * L::KRow + kq * (D / 2);
-    *(u32x4_t*)(dst + e * 16) = mx_decode8(x.k.w[e], __uint_as_float(x.ks[D == 256 ? e >> 2 : 0] << 23));
+  auto store_k = [&](const Raw& x, int buf, int e) __attribute__((always_inline)) {  // piece e of KE / 8
+    uint8_t* dst = smem + buf * L::K + (grp * 16 + kt) * L::KRow + k0 * 2;
+    *(u32x4_t*)(dst + e * 16) = mx_decode8(x.k.w[e], __uint_as_float(x.ks[KE > 32 ? e >> 2 : 0] << 23));
   };
   // V by element. The products must not meet a NaN: 0 * NaN would reach rows that do not
   // see it. NaN blocks go in as zeros (scale 0) and are marked; tokens past the last and on
   // pages that are not there may hold anything and go in under scale 0 too.
   auto mark_v = [&](Raw& x, int buf, int tile, const Pages& pg) __attribute__((always_inline)) {
-    const int t0 = tile * kTile + wave * 16;
-    if ((t0 + 16 > rows.kv_len) | ((pg.there >> wave & 1u) == 0)) {
+    const int t0 = tile * kTile + grp * 16;
+    if ((t0 + 16 > rows.kv_len) | ((pg.there >> grp & 1u) == 0)) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        x.vs[i] = ((t0 + 4 * vq + i < rows.kv_len) & ((pg.there >> wave & 1u) != 0)) ? x.vs[i] : 0u;
+        x.vs[i] = ((t0 + 4 * vq + i < rows.kv_len) & ((pg.there >> grp & 1u) != 0)) ? x.vs[i] : 0u;
     }
     const uint32_t most = max(max(x.vs[0], x.vs[1]), max(x.vs[2], x.vs[3]));
     const uint32_t any = __any(most == 255u);
+    uint32_t marks = 0;
     if (any) {
-      uint32_t marks = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         marks |= x.vs[i] == 255u ? 1u << (8 * i) : 0u;
         x.vs[i] = x.vs[i] == 255u ? 0u : x.vs[i];
       }
-      *(uint32_t*)(smem + L::NanAt + buf * L::Nan + vblk * kTile + wave * 16 + 4 * vq) = marks;  // the same from a block's lanes
     }
-    *(uint32_t*)(smem + L::FlagAt + (buf * kWaves + wave) * 4) = any;
+    if (any || H > 1) {  // of parts, the one without marks says so
+      *(uint32_t*)(smem + L::NanAt + buf * L::Nan + vblk * kTile + grp * 16 + 4 * vq) = marks;  // the same from a block's lanes
+    }
+    *(uint32_t*)(smem + L::FlagAt + (buf * 8 + wave) * 4) = any;
   };
   auto store_v = [&](const Raw& x, int buf, int d) __attribute__((always_inline)) {  // elements 2 d, 2 d + 1 of the lane's
     // tokens 4 vq .. + 3 of the 16: lane half vq & 1, first or second four
     uint8_t* dst = smem + L::VAt + buf * L::V + (vq >> 1) * 8;
-    const int c = 2 * wave + (vq & 1), e = vc * (D / 16) + 2 * d;
+    const int c = 2 * grp + (vq & 1), e = v0 + 2 * d;
     uint32_t two[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) two[i] = decode2(x.v[i][D == 256 ? d >> 2 : 0], __uint_as_float(x.vs[i] << 23), d & 3);
+    for (int i = 0; i < 4; ++i) two[i] = decode2(x.v[i][VE > 8 ? d >> 2 : 0], __uint_as_float(x.vs[i] << 23), d & 3);
     *(u32x2_t*)(dst + e * 128 + v_chunk(e, c) * 16) =
         u32x2_t{__builtin_amdgcn_perm(two[1], two[0], 0x05040100u), __builtin_amdgcn_perm(two[3], two[2], 0x05040100u)};
     *(u32x2_t*)(dst + (e + 1) * 128 + v_chunk(e + 1, c) * 16) =
@@ -319,7 +328,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : 1) void mx_attention_pro
   };
   // The phases, in steps of RB matrix instructions each with its share of the rest, fenced so
   // that the order stands: left alone the instructions gather by kind, and one wave a SIMD
-  // then does first the one and then the other.
+  // then does first the one and then the other (D = 256: 196 us for 188).
   auto fence = []() __attribute__((always_inline)) { __builtin_amdgcn_sched_barrier(0); };
   auto phase_scores = [&](f32x16_t (&x)[RB], const f32x16_t (&y)[RB], int vbuf, int half) __attribute__((always_inline)) {
     constexpr int G = 4 * RB;  // groups of weights, over KS steps; packed a step after they are taken
@@ -341,11 +350,15 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : 1) void mx_attention_pro
 
   // Marked blocks: a product of "is NaN" with "is seen" tells the rows that get one, for the
   // whole block of 32 elements at once.
-  u32x4_t flag;  // of V[t], one word a wave
+  u32x4_t flag;  // of V[t], one word for 16 tokens
+  auto read_flag = [&](int buf) __attribute__((always_inline)) {
+    flag = *(const u32x4_t*)(smem + L::FlagAt + buf * 32);
+    if constexpr (H == 2) flag |= *(const u32x4_t*)(smem + L::FlagAt + buf * 32 + 16);
+  };
   auto nans = [&](int buf, int tile, uint32_t there) __attribute__((always_inline)) {
     if (__builtin_amdgcn_readfirstlane(flag[0] | flag[1] | flag[2] | flag[3]) == 0) return;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {  // wave k's tokens
+    for (int k = 0; k < 4; ++k) {
       if (__builtin_amdgcn_readfirstlane(flag[k]) == 0) continue;
       bf16x8_t seen[RB];
 #pragma unroll
@@ -393,13 +406,13 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : 1) void mx_attention_pro
     load_k(x, at);
     load_v(x, at);
 #pragma unroll
-    for (int d = 0; d < DB; ++d) store_k(x, 0, d);
+    for (int d = 0; d < KE / 8; ++d) store_k(x, 0, d);
     mark_v(x, 0, tile, at);
 #pragma unroll
-    for (int d = 0; d < DB; ++d) store_v(x, 0, d);
+    for (int d = 0; d < VE / 2; ++d) store_v(x, 0, d);
     load_k(x, an);
 #pragma unroll
-    for (int d = 0; d < DB; ++d) store_k(x, 1, d);
+    for (int d = 0; d < KE / 8; ++d) store_k(x, 1, d);
     load_v(x, an);
     load_k(x, af);
     barrier();
@@ -411,7 +424,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : 1) void mx_attention_pro
     mask(s0, tile, 0, at.there);
 #pragma unroll
     for (int k = 0; k < KS; ++k) read_k(0, 1, k);
-    flag = *(const u32x4_t*)(smem + L::FlagAt);
+    read_flag(0);
     auto body = [&](int i, auto buffer) __attribute__((always_inline)) {
       constexpr int buf = decltype(buffer)::value;
       nans(buf, tile, at.there);
@@ -429,13 +442,13 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : 1) void mx_attention_pro
         values(k);
         read_k(buf ^ 1, 0, k);
         if (k == 0) mark_v(x, buf ^ 1, next, an);
-        if (k & 1) store_v(x, buf ^ 1, k >> 1);
+        if ((k & 1) && (k >> 1) < VE / 2) store_v(x, buf ^ 1, k >> 1);
         fence();
       }
       load_v(x, af);
       barrier();
       // 3
-      flag = *(const u32x4_t*)(smem + L::FlagAt + (buf ^ 1) * kWaves * 4);
+      read_flag(buf ^ 1);
       fence();
       phase_scores(s0, s1, buf, 1);
       settle(s1);
@@ -446,7 +459,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : 1) void mx_attention_pro
       for (int k = 0; k < KS; ++k) {
         values(k);
         read_k(buf ^ 1, 1, k);
-        if (k & 1) store_k(x, buf, k >> 1);
+        if ((k & 1) && (k >> 1) < KE / 8) store_k(x, buf, k >> 1);
         fence();
       }
       load_k(x, ab);
@@ -497,33 +510,39 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : 1) void mx_attention_pro
   }
 }
 
-template <int D, int RB>
+template <int D>
+struct Form {
+  static constexpr int RB = D == 64 ? 2 : 1, W = D == 128 ? 8 : 4;
+};
+
+template <int D, int RB = Form<D>::RB, int W = Form<D>::W>
 hipError_t launch_prompt(const MxAttnArgs& a, hipStream_t stream) {
-  const int64_t tiles = a.b.tokens * a.group / (32 * RB * kWaves) + a.b.batch;
-  mx_attention_prompt_kernel<D, RB>
-      <<<dim3((unsigned)(tiles * a.c.kv_heads), a.splits), 64 * kWaves, Lds<D>::Bytes, stream>>>(a);
+  const int64_t tiles = a.b.tokens * a.group / (32 * RB * W) + a.b.batch;
+  mx_attention_prompt_kernel<D, RB, W>
+      <<<dim3((unsigned)(tiles * a.c.kv_heads), a.splits), 64 * W, Lds<D>::Bytes, stream>>>(a);
   return hipGetLastError();
+}
+
+template <int D, int RB = Form<D>::RB, int W = Form<D>::W>
+hipError_t setup_prompt() {
+  return hipFuncSetAttribute((const void*)mx_attention_prompt_kernel<D, RB, W>,
+                             hipFuncAttributeMaxDynamicSharedMemorySize, Lds<D>::Bytes);
 }
 
 }  // namespace
 
 hipError_t mx_attention_setup() {
-  hipError_t e = hipFuncSetAttribute((const void*)mx_attention_prompt_kernel<64, 2>,
-                                     hipFuncAttributeMaxDynamicSharedMemorySize, Lds<64>::Bytes);
-  if (e == hipSuccess)
-    e = hipFuncSetAttribute((const void*)mx_attention_prompt_kernel<128, 2>,
-                            hipFuncAttributeMaxDynamicSharedMemorySize, Lds<128>::Bytes);
-  if (e == hipSuccess)
-    e = hipFuncSetAttribute((const void*)mx_attention_prompt_kernel<256, 1>,
-                            hipFuncAttributeMaxDynamicSharedMemorySize, Lds<256>::Bytes);
+  hipError_t e = setup_prompt<64>();
+  if (e == hipSuccess) e = setup_prompt<128>();
+  if (e == hipSuccess) e = setup_prompt<256>();
   return e;
 }
 
 hipError_t launch_mx_attention_prompt(const MxAttnArgs& a, hipStream_t stream) {
   switch (a.c.head_dim) {
-    case 64: return launch_prompt<64, 2>(a, stream);
-    case 128: return launch_prompt<128, 2>(a, stream);
-    default: return launch_prompt<256, 1>(a, stream);
+    case 64: return launch_prompt<64>(a, stream);
+    case 128: return launch_prompt<128>(a, stream);
+    default: return launch_prompt<256>(a, stream);
   }
 }
 
