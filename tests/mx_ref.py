@@ -87,9 +87,12 @@ def attention(q, k, v, scale, causal=True, window=0, sinks=0, hidden=None):
     hidden: bool [t], tokens that no row sees. The tolerance of o_d = sum_t w_t v_td against the
     library's arithmetic: scores are fp32 sums of exact products (d + 2 roundings of 2^-23 of
     sum |q||k|), which moves weights by that much, relatively, twice (numerator and sum); the
-    weights are rounded to bf16 (2^-8) for the product; exp2, its argument and the fp32 sums
-    over t stay within 2^-15 (arguments up to 2^6 in fp32: 2^-18, thousands of additions with
-    2^-24 each); the output is rounded once (2^-8). A weight below the smallest normal fp32 number
+    weights are rounded to bf16, w_t (1 + e_t) with |e_t| <= 2^-8, for the product and for their
+    sum: sum w (1 + e) v / sum w (1 + e) - o = sum w e (v - o) / sum w (1 + e), at most
+    2^-8 (sum w |v| + |o|) beside terms of 2^-16; exp2, its argument and the fp32 sums over t
+    stay within 2^-15, those terms with them within 2^-14 (arguments up to 2^6 in fp32: 2^-18,
+    thousands of additions with 2^-24 each); the output is rounded once (2^-8). A weight below
+    the smallest normal fp32 number
     may become 0: an error of at most 2^-126 beside a sum of weights of at least 1 (the running
     maximum never exceeds the largest score, whose weight is then at least 1), so at most
     2^-126 |v_td| of each token, and as much again for a product of o that falls below it."""
@@ -117,7 +120,7 @@ def attention(q, k, v, scale, causal=True, window=0, sinks=0, hidden=None):
             mag = float((kk.abs() @ q[i, j].abs() * scale).max())
             w = torch.softmax(s, 0)
             o[i, j] = w @ vv
-            err = 2.0 ** -8 + 2 * (d + 2) * 2.0 ** -23 * mag + 2.0 ** -15
+            err = 2.0 ** -8 + 2.0 ** -14 + 2 * (d + 2) * 2.0 ** -23 * mag
             tiny = 2.0 ** -126 * (vv.abs().sum(0) + vv.shape[0])
-            tol[i, j] = err * (w @ vv.abs()) + 2.0 ** -8 * o[i, j].abs() + tiny
+            tol[i, j] = err * (w @ vv.abs()) + 2 * 2.0 ** -8 * o[i, j].abs() + tiny
     return o, tol
