@@ -30,16 +30,21 @@ struct MxAttnPlan {
 
 // Rows: the packed rows (rows x heads of a group) of an average sequence. Up to 64 of them
 // (32 at head_dim 256) are one workgroup's of the few-rows form, whose four waves split the
-// tokens; beyond that the prompt form gives every wave rows of its own.
-// Splits: where the rows alone do not give enough workgroups, pieces of the token axis do,
-// but at least kMinTiles 32-token tiles a wave, so that a split is more than its own start
-// and its share of the join. Few rows: 8 workgroups for each of the 256 CUs (ragged lengths
-// then even out over two rounds of them: 48 tokens over up to 8200 take 92 us with 5 splits,
-// 108 with 2, 97 with 8). Prompts: their workgroups are long and one fills a CU, and a split
-// writes and reads every row once more in fp32, so only what leaves CUs idle is split.
+// tokens; beyond that the prompt form gives every wave 32 rows of its own.
+//
+// Splits: where the rows alone do not give enough workgroups, pieces of the token axis do.
+// Few rows: 8 workgroups for each of the 256 CUs (ragged lengths then even out over two
+// rounds of them: 48 tokens over up to 8200 take 92 us with 5 splits, 108 with 2, 97 with 8),
+// but at least two 32-token tiles a wave, so that a split is more than its own start.
+// Prompts: as many as are resident at once, by registers 3, 2 or 1 a CU. But a split writes
+// and reads every row once more in fp32, head_dim tokens heads splits * 4 ps as measured,
+// which it has to save of the head_dim / 6 ns that a workgroup takes for a token: the sum is
+// least at sqrt(40 seen / (tokens heads)) splits, and below three of them not splitting is as
+// good. Measured, 32 heads of 128 over 8: 256 rows over 8192 take 177 us whole, 71 with 6
+// splits, 62 with 8, 71 with 16; over 2048: 51, with 3 splits 42, with 4 46; 1024 rows over
+// 1024: 33 whole, 72 with 2.
 inline MxAttnPlan mx_attention_plan(int64_t tokens, int64_t batch, int64_t heads, int64_t kv_heads, int64_t head_dim,
                                     int64_t max_kv, int64_t window, int64_t sinks) {
-  constexpr int64_t kMinTiles = 2;
   MxAttnPlan p{true, 1, 1};
   if (tokens <= 0 || batch <= 0) return p;
   const int64_t group = heads / kv_heads;
@@ -47,17 +52,25 @@ inline MxAttnPlan mx_attention_plan(int64_t tokens, int64_t batch, int64_t heads
   const int most = head_dim == 256 ? 2 : 4;
   p.few = rows <= 16 * most;
   p.row_tiles = rows <= 16 ? 1 : rows <= 32 ? 2 : most;
-  const int64_t per_group = p.few ? 16 * p.row_tiles : head_dim == 256 ? 128 : 256;
+  const int64_t per_group = p.few ? 16 * p.row_tiles : 128;
   int64_t tiles = (tokens * group + per_group - 1) / per_group;
   if (tiles < batch) tiles = batch;
   const int64_t groups = tiles * kv_heads;
-  int64_t seen = max_kv;
-  if (window > 0) {  // a row tile's span: the window, its rows, the first tokens
+  int64_t seen = max_kv < (1 << 30) ? max_kv : 1 << 30;  // no sequence is longer
+  if (window > 0 && window < seen && sinks < seen) {     // a row tile's span: the window, its rows, the first tokens
     const int64_t w = window + per_group / group + sinks;
     if (w < seen) seen = w;
   }
-  const int64_t most_splits = seen / (32 * kMinTiles * 4);
-  int64_t s = p.few ? 2048 / groups : 256 / groups;
+  int64_t s, most_splits;
+  if (p.few) {
+    s = 2048 / groups;
+    most_splits = seen / (2 * 32 * 4);
+  } else {
+    s = (head_dim == 64 ? 768 : head_dim == 128 ? 512 : 256) / groups;
+    most_splits = 2;
+    while ((most_splits + 1) * (most_splits + 1) * tokens * heads <= 40 * seen && most_splits < kMxMostSplits) ++most_splits;
+    if (most_splits < 3) most_splits = 1;
+  }
   if (s > most_splits) s = most_splits;
   if (s > kMxMostSplits) s = kMxMostSplits;
   p.splits = s < 1 ? 1 : (int)s;

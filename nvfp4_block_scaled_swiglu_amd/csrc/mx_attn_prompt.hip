@@ -4,10 +4,10 @@
 //
 // What bounds it is the issue of instructions: the two matrix products, one exp2 per score
 // and the rounding of its result, and the reads from LDS go side by side (taking any one of
-// them out gains less than a tenth). A workgroup has 256 packed rows (D = 256: 128), 32 RB to
-// a wave, and walks the tokens 64 at a time. A tile's codes are decoded once for the
-// workgroup, into bf16 in LDS, and the products run on v_mfma_f32_32x32x16_bf16 in the
-// transposed form, lane (n, h) = (lane & 31, lane >> 5):
+// them out gains less than a tenth). A workgroup has 128 packed rows, 32 to a wave, and walks
+// the tokens 64 at a time. A tile's codes are decoded once for the workgroup, into bf16 in
+// LDS, and the products run on v_mfma_f32_32x32x16_bf16 in the transposed form, lane
+// (n, h) = (lane & 31, lane >> 5):
 //
 //   S^T = K Q^T    A: token n, elements 16 s + 8 h .. + 7 of step s, a 16-byte LDS read.
 //                  S^T comes out with lane (n, h) holding packed row n and, of 32 tokens,
@@ -16,13 +16,15 @@
 //                  tokens of step s. A: element n of a block of 32, the same 8 tokens - V is
 //                  laid in LDS by element with its tokens in that order, again one read.
 //
-// Each wave reads the whole tile from LDS for its 32 RB rows. Measured, 4,096 tokens, 32 heads
-// over 8, twice, D = 64: four waves of 64 rows 205 us, two workgroups a CU; eight of 32 rows
-// 245 us. 1,500 tokens, four times, D = 128: eight waves of 32 rows, two a SIMD, 125 us; four
-// of 64 rows, one a SIMD, 151 us. D = 256 has registers for neither and takes four of 32.
-// Either way waves are few, so overlap comes from the instruction stream. A tile goes in two
-// halves of 32 tokens, each in two phases of RB D / 16 matrix instructions beside what else
-// is due:
+// Each wave reads the whole tile from LDS for its 32 rows. 64 rows to a wave would halve
+// that, and eight waves the decoding; but then a CU has one or two workgroups where it has
+// two or three, with nothing to run beside a barrier or a workgroup's start. Measured, 56
+// heads of 128 over 8, 2 ragged prompts: 787 us, eight waves 802, 64 rows 1171. 32 heads over
+// 8, 1,500 tokens eight times: 213 us and eight waves 227; of 64, 139 us and 64 rows 158 (they
+// gain from 4,096 tokens on only, 9 % at most).
+// Waves are few all the same, so overlap comes from the instruction stream as well. A tile
+// goes in two halves of 32 tokens, each in two phases of D / 16 matrix instructions beside
+// what else is due:
 //
 //   1  S1 = K[t]1 Q       ||  P = exp2(S0)                  ||  read V[t]0
 //   2  O += V[t]0 P       ||  decode V[t + 1] into LDS      ||  read K[t + 1]0   | barrier
@@ -45,6 +47,7 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kTile = 64;  // tokens per step
+constexpr int kWaves = 4, kRows = 32 * kWaves;
 
 // A raise is due when the weights of a lane's 16 tokens add up to more: some weight is then
 // above 2^8, and none that passes is above 2^12.
@@ -61,16 +64,16 @@ struct Lds {
   static constexpr int KRow = D * 2 + 16;
   static constexpr int K = kTile * KRow, V = D * kTile * 2;   // bytes of a tile
   static constexpr int Nan = D / 32 * kTile;                  // V bytes that are NaN, [block][token]
-  static constexpr int VAt = 2 * K, NanAt = VAt + 2 * V, FlagAt = NanAt + 2 * Nan, Bytes = FlagAt + 2 * 4 * 8;
+  static constexpr int VAt = 2 * K, NanAt = VAt + 2 * V, FlagAt = NanAt + 2 * Nan, Bytes = FlagAt + 2 * 4 * kWaves;
   static_assert(Bytes <= 160 * 1024, "LDS");
 };
 
-template <int D, int RB, int kWaves>
-__global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : kWaves / 4) void mx_attention_prompt_kernel(MxAttnArgs a) {
+constexpr int waves_per_simd(int d) { return d == 64 ? 3 : d == 128 ? 2 : 1; }  // by registers
+
+template <int D>
+__global__ __launch_bounds__(64 * kWaves, waves_per_simd(D)) void mx_attention_prompt_kernel(MxAttnArgs a) {
   using L = Lds<D>;
   constexpr int KS = D / 16, DB = D / 32;
-  constexpr int H = kWaves / 4;  // waves that share 16 tokens of a tile, each a part of the elements
-  constexpr int kRows = 32 * RB * kWaves;
   extern __shared__ __align__(16) uint8_t smem[];
 
   const int lane = threadIdx.x & 63;
@@ -89,38 +92,34 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : kWaves / 4) void mx_atte
   const int end = (int)((int64_t)span.count * (split + 1) / a.splits);
 
   // ---- the wave's rows ----
-  const int p0 = rows.first + wave * 32 * RB;
-  const int p1 = p0 + 32 * RB < rows.count ? p0 + 32 * RB : rows.count;
+  const int p0 = rows.first + wave * 32;
+  const int p1 = p0 + 32 < rows.count ? p0 + 32 : rows.count;
   MxSight sight{0, 0, 0, 0, 0};  // a wave without rows sees nothing
   if (p0 < p1) sight = mx_sight(a, rows, p0, p1);
-  if (p1 - p0 < 32 * RB) sight.high_min = 0;
-  bf16x8_t q[RB][KS];
-  int high[RB], low[RB];
-#pragma unroll
-  for (int r = 0; r < RB; ++r) {
-    const int p = p0 + r * 32 + n;
-    const bool real = p < rows.count;
-    const int i = p / g;
-    const uint16_t* src = a.q + (rows.r0 + i) * a.q_token + (int64_t)(kvh * g + p % g) * a.q_head + 8 * h;
+  if (p1 - p0 < 32) sight.high_min = 0;
+  const int pn = p0 + n;
+  const bool real = pn < rows.count;
+  bf16x8_t q[KS];
+  {
+    const uint16_t* src = a.q + (rows.r0 + pn / g) * a.q_token + (int64_t)(kvh * g + pn % g) * a.q_head + 8 * h;
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
       u32x4_t w = {0u, 0u, 0u, 0u};
       if (real) w = *(const u32x4_t*)(src + 16 * s);
-      q[r][s] = as_bf16x8(w[0], w[1], w[2], w[3]);
+      q[s] = as_bf16x8(w[0], w[1], w[2], w[3]);
     }
-    high[r] = real ? mx_high(a, rows.kv_len, rows.back + i) : 0;
-    low[r] = mx_low(a, rows.back + i);
   }
+  const int high = real ? mx_high(a, rows.kv_len, rows.back + pn / g) : 0;
+  const int low = mx_low(a, rows.back + pn / g);
 
-  // ---- a tile's way into LDS: wave w brings tokens 16 (w % 4) .. + 15, part w / 4 of H ----
-  // K: four lanes to a token, D / 4 / H elements each; V: D / 16 / H elements of four tokens
-  constexpr int KE = D / 4 / H, VE = D / 16 / H;  // elements of a lane
-  const int grp = wave & 3, part = wave >> 2;
-  const int kt = lane >> 2, k0 = (part * 4 + (lane & 3)) * KE;
-  const int vq = (lane >> 4 & 1) * 2 + (lane >> 5), v0 = (part * 16 + (lane & 15)) * VE;
+  // ---- a tile's way into LDS: wave w brings tokens 16 w .. + 15 ----
+  // K: four lanes to a token, D / 4 elements each; V: D / 16 elements of four tokens
+  constexpr int KE = D / 4, VE = D / 16;  // elements of a lane
+  const int kt = lane >> 2, k0 = (lane & 3) * KE;
+  const int vq = (lane >> 4 & 1) * 2 + (lane >> 5), v0 = (lane & 15) * VE;
   const int vblk = v0 / 32;
   struct Raw {
-    Words<(KE >= 8 ? KE / 8 : 1)> k;
+    Words<KE / 8> k;
     uint32_t ks[KE > 32 ? 2 : 1];
     uint32_t v[4][VE > 8 ? 2 : 1];
     uint32_t vs[4];
@@ -151,12 +150,12 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : kWaves / 4) void mx_atte
       for (int w = 0; w < 4; ++w)
         if (__builtin_amdgcn_readlane(entry, ((t + 16 * w) >> a.b.page_shift) - base) < 0) x.there &= ~(1u << w);
     }
-    x.row = mx_cache_row(a, __builtin_amdgcn_readlane(entry, ((t + 16 * grp) >> a.b.page_shift) - base), kvh,
-                         t + 16 * grp);
+    x.row = mx_cache_row(a, __builtin_amdgcn_readlane(entry, ((t + 16 * wave) >> a.b.page_shift) - base), kvh,
+                         t + 16 * wave);
     return x;
   };
   auto load_k = [&](Raw& x, const Pages& pg) __attribute__((always_inline)) {
-    x.k = load_words<(KE >= 8 ? KE / 8 : 1)>(a.c.k_codes + pg.row * (D / 2) + (kt * (D / 2) + k0 / 2));
+    x.k = load_words<KE / 8>(a.c.k_codes + pg.row * (D / 2) + (kt * (D / 2) + k0 / 2));
     const uint8_t* s = a.c.k_scales + pg.row * (D / 32) + (kt * (D / 32) + k0 / 32);
 #pragma unroll
     for (int b = 0; b < (KE > 32 ? 2 : 1); ++b) x.ks[b] = s[b];
@@ -165,8 +164,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : kWaves / 4) void mx_atte
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint8_t* p = a.c.v_codes + pg.row * (D / 2) + ((4 * vq + i) * (D / 2) + v0 / 2);
-      if constexpr (VE == 2) x.v[i][0] = *p;
-      else if constexpr (VE == 4) x.v[i][0] = *(const uint16_t*)p;
+      if constexpr (VE == 4) x.v[i][0] = *(const uint16_t*)p;
       else {
         const Words<VE / 8> w = load_words<VE / 8>(p);
 #pragma unroll
@@ -176,38 +174,36 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : kWaves / 4) void mx_atte
     }
   };
   auto store_k = [&](const Raw& x, int buf, int e) __attribute__((always_inline)) {  // piece e of KE / 8
-    uint8_t* dst = smem + buf * L::K + (grp * 16 + kt) * L::KRow + k0 * 2;
+    uint8_t* dst = smem + buf * L::K + (wave * 16 + kt) * L::KRow + k0 * 2;
     *(u32x4_t*)(dst + e * 16) = mx_decode8(x.k.w[e], __uint_as_float(x.ks[KE > 32 ? e >> 2 : 0] << 23));
   };
   // V by element. The products must not meet a NaN: 0 * NaN would reach rows that do not
   // see it. NaN blocks go in as zeros (scale 0) and are marked; tokens past the last and on
   // pages that are not there may hold anything and go in under scale 0 too.
   auto mark_v = [&](Raw& x, int buf, int tile, const Pages& pg) __attribute__((always_inline)) {
-    const int t0 = tile * kTile + grp * 16;
-    if ((t0 + 16 > rows.kv_len) | ((pg.there >> grp & 1u) == 0)) {
+    const int t0 = tile * kTile + wave * 16;
+    if ((t0 + 16 > rows.kv_len) | ((pg.there >> wave & 1u) == 0)) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        x.vs[i] = ((t0 + 4 * vq + i < rows.kv_len) & ((pg.there >> grp & 1u) != 0)) ? x.vs[i] : 0u;
+        x.vs[i] = ((t0 + 4 * vq + i < rows.kv_len) & ((pg.there >> wave & 1u) != 0)) ? x.vs[i] : 0u;
     }
     const uint32_t most = max(max(x.vs[0], x.vs[1]), max(x.vs[2], x.vs[3]));
     const uint32_t any = __any(most == 255u);
-    uint32_t marks = 0;
     if (any) {
+      uint32_t marks = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         marks |= x.vs[i] == 255u ? 1u << (8 * i) : 0u;
         x.vs[i] = x.vs[i] == 255u ? 0u : x.vs[i];
       }
+      *(uint32_t*)(smem + L::NanAt + buf * L::Nan + vblk * kTile + wave * 16 + 4 * vq) = marks;  // the same from a block's lanes
     }
-    if (any || H > 1) {  // of parts, the one without marks says so
-      *(uint32_t*)(smem + L::NanAt + buf * L::Nan + vblk * kTile + grp * 16 + 4 * vq) = marks;  // the same from a block's lanes
-    }
-    *(uint32_t*)(smem + L::FlagAt + (buf * 8 + wave) * 4) = any;
+    *(uint32_t*)(smem + L::FlagAt + (buf * 4 + wave) * 4) = any;
   };
   auto store_v = [&](const Raw& x, int buf, int d) __attribute__((always_inline)) {  // elements 2 d, 2 d + 1 of the lane's
     // tokens 4 vq .. + 3 of the 16: lane half vq & 1, first or second four
     uint8_t* dst = smem + L::VAt + buf * L::V + (vq >> 1) * 8;
-    const int c = 2 * grp + (vq & 1), e = v0 + 2 * d;
+    const int c = 2 * wave + (vq & 1), e = v0 + 2 * d;
     uint32_t two[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) two[i] = decode2(x.v[i][VE > 8 ? d >> 2 : 0], __uint_as_float(x.vs[i] << 23), d & 3);
@@ -218,18 +214,13 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : kWaves / 4) void mx_atte
   };
 
   // ---- state ----
-  f32x16_t o[RB][DB];
-  f32x16_t s0[RB], s1[RB];  // scores of a tile's halves
-  float m[RB], l[RB];
+  f32x16_t o[DB];
+  f32x16_t s0, s1;  // scores of a tile's halves
+  float m = -INFINITY, l = 0.0f;
 #pragma unroll
-  for (int r = 0; r < RB; ++r) {
-    m[r] = -INFINITY;
-    l[r] = 0.0f;
+  for (int d = 0; d < DB; ++d)
 #pragma unroll
-    for (int d = 0; d < DB; ++d)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[r][d][i] = 0.0f;
-  }
+    for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
   bool fresh = true;  // some row has seen nothing yet
 
   bf16x8_t kf[KS], vf[KS];  // fragments of a half: K by step, V by (16 tokens, block)
@@ -240,98 +231,78 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : kWaves / 4) void mx_atte
     const int e = k % DB * 32 + n;
     vf[k] = *(const bf16x8_t*)(smem + L::VAt + buf * L::V + e * 128 + v_chunk(e, 4 * half + 2 * (k / DB) + h) * 16);
   };
-  auto zero = [&](f32x16_t (&x)[RB]) __attribute__((always_inline)) {
+  auto zero = [&](f32x16_t& x) __attribute__((always_inline)) {
 #pragma unroll
-    for (int r = 0; r < RB; ++r)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) x[r][i] = 0.0f;
+    for (int i = 0; i < 16; ++i) x[i] = 0.0f;
   };
-  auto scores = [&](f32x16_t (&x)[RB], int k) __attribute__((always_inline)) {  // step k
-#pragma unroll
-    for (int r = 0; r < RB; ++r) x[r] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[k], q[r][k], x[r], 0, 0, 0);
+  auto scores = [&](f32x16_t& x, int k) __attribute__((always_inline)) {  // step k
+    x = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[k], q[k], x, 0, 0, 0);
   };
   // (no short-circuits: selects, not branches around the accumulators)
-  auto sees = [&](int r, int t, uint32_t there, int group) __attribute__((always_inline)) {
-    return (t < high[r]) & ((t >= low[r]) | (t < sight.sinks)) & ((there >> group & 1u) != 0);
+  auto sees = [&](int t, uint32_t there, int group) __attribute__((always_inline)) {
+    return (t < high) & ((t >= low) | (t < sight.sinks)) & ((there >> group & 1u) != 0);
   };
   // register i of a half is its token 8 (i / 4) + 4 h + i % 4
-  auto mask = [&](f32x16_t (&x)[RB], int tile, int half, uint32_t there) __attribute__((always_inline)) {
+  auto mask = [&](f32x16_t& x, int tile, int half, uint32_t there) __attribute__((always_inline)) {
     const int t0 = tile * kTile + half * 32;
     if ((there >> (2 * half) & 3u) == 3u && t0 + 32 <= sight.high_min &&
         (t0 >= sight.low_max || t0 + 32 <= sight.sinks))
       return;
 #pragma unroll
-    for (int r = 0; r < RB; ++r)
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        x[r][i] = sees(r, t0 + 8 * (i >> 2) + 4 * h + (i & 3), there, 2 * half + (i >> 3)) ? x[r][i] : -INFINITY;
+    for (int i = 0; i < 16; ++i)
+      x[i] = sees(t0 + 8 * (i >> 2) + 4 * h + (i & 3), there, 2 * half + (i >> 3)) ? x[i] : -INFINITY;
   };
-  bf16x8_t pf[RB][2];
-  uint32_t pw[RB][8];  // the weights, packed
-  float sum[RB];       // of the lane's 16
-  // weights 4 j .. 4 j + 3 of row block j / 4: taken (the exponentials), then summed and packed
-  auto take = [&](const f32x16_t (&x)[RB], int j, float (&p)[4]) __attribute__((always_inline)) {
-    const int r = j >> 2;
-    const float neg = m[r] == -INFINITY ? 0.0f : -m[r];  // nothing seen yet: every weight is exp2(-inf)
+  uint32_t pw[8];  // the weights, packed
+  float sum;       // of the lane's 16
+  // weights 4 j .. 4 j + 3: taken (the exponentials), then summed and packed
+  auto take = [&](const f32x16_t& x, int j, float (&p)[4]) __attribute__((always_inline)) {
+    const float neg = m == -INFINITY ? 0.0f : -m;  // nothing seen yet: every weight is exp2(-inf)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[r][4 * (j & 3) + i], a.scale_log2, neg));
+    for (int i = 0; i < 4; ++i) p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[4 * j + i], a.scale_log2, neg));
   };
   auto add = [&](int j, const float (&p)[4]) __attribute__((always_inline)) {
-    const int r = j >> 2;
     const uint32_t w0 = pack_bf16(p[0], p[1]), w1 = pack_bf16(p[2], p[3]);
     const bf16x2_t one = as_bf16x2(0x3F803F80u);
-    const float t = __builtin_amdgcn_fdot2_f32_bf16(as_bf16x2(w0), one, (j & 3) == 0 ? 0.0f : sum[r], false);
-    sum[r] = __builtin_amdgcn_fdot2_f32_bf16(as_bf16x2(w1), one, t, false);
-    pw[r][2 * (j & 3)] = w0;
-    pw[r][2 * (j & 3) + 1] = w1;
+    const float t = __builtin_amdgcn_fdot2_f32_bf16(as_bf16x2(w0), one, j == 0 ? 0.0f : sum, false);
+    sum = __builtin_amdgcn_fdot2_f32_bf16(as_bf16x2(w1), one, t, false);
+    pw[2 * j] = w0;
+    pw[2 * j + 1] = w1;
   };
   // after the weights of x: raises the maximum and takes them again if that is due
-  auto settle = [&](const f32x16_t (&x)[RB]) __attribute__((always_inline)) {
-    bool due = fresh;
+  bf16x8_t pf[2];
+  auto settle = [&](const f32x16_t& x) __attribute__((always_inline)) {
+    if (__any(fresh | !(sum <= kMostSum))) {
+      float top = x[0];
 #pragma unroll
-    for (int r = 0; r < RB; ++r) due |= !(sum[r] <= kMostSum);
-    if (__any(due)) {
-      bool none = false;
+      for (int i = 1; i < 16; ++i) top = fmaxf(top, x[i]);
+      top *= a.scale_log2;
+      const float next = fmaxf(m, fmaxf(top, __shfl_xor(top, 32, 64)));
+      const float f = m == next ? 1.0f : __builtin_amdgcn_exp2f(m - next);  // m = -inf: o and l are 0
+      m = next;
+      fresh = __any((next == -INFINITY) & (high > 0));
+      l *= f;
 #pragma unroll
-      for (int r = 0; r < RB; ++r) {
-        float top = x[r][0];
+      for (int d = 0; d < DB; ++d) o[d] *= f;
 #pragma unroll
-        for (int i = 1; i < 16; ++i) top = fmaxf(top, x[r][i]);
-        top *= a.scale_log2;
-        const float next = fmaxf(m[r], fmaxf(top, __shfl_xor(top, 32, 64)));
-        const float f = m[r] == next ? 1.0f : __builtin_amdgcn_exp2f(m[r] - next);  // m = -inf: o and l are 0
-        m[r] = next;
-        none |= (next == -INFINITY) & (high[r] > 0);
-        l[r] *= f;
-#pragma unroll
-        for (int d = 0; d < DB; ++d) o[r][d] *= f;
-      }
-      fresh = __any(none);
-#pragma unroll
-      for (int j = 0; j < 4 * RB; ++j) {
+      for (int j = 0; j < 4; ++j) {
         float p[4];
         take(x, j, p);
         add(j, p);
       }
     }
+    l += sum;
 #pragma unroll
-    for (int r = 0; r < RB; ++r) {
-      l[r] += sum[r];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) pf[r][k] = as_bf16x8(pw[r][4 * k], pw[r][4 * k + 1], pw[r][4 * k + 2], pw[r][4 * k + 3]);
-    }
+    for (int k = 0; k < 2; ++k) pf[k] = as_bf16x8(pw[4 * k], pw[4 * k + 1], pw[4 * k + 2], pw[4 * k + 3]);
   };
   auto values = [&](int k) __attribute__((always_inline)) {  // 16 tokens k / DB, block k % DB
-#pragma unroll
-    for (int r = 0; r < RB; ++r)
-      o[r][k % DB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[k], pf[r][k / DB], o[r][k % DB], 0, 0, 0);
+    o[k % DB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[k], pf[k / DB], o[k % DB], 0, 0, 0);
   };
-  // The phases, in steps of RB matrix instructions each with its share of the rest, fenced so
+  // The phases, in steps of a matrix instruction each with its share of the rest, fenced so
   // that the order stands: left alone the instructions gather by kind, and one wave a SIMD
   // then does first the one and then the other (D = 256: 196 us for 188).
   auto fence = []() __attribute__((always_inline)) { __builtin_amdgcn_sched_barrier(0); };
-  auto phase_scores = [&](f32x16_t (&x)[RB], const f32x16_t (&y)[RB], int vbuf, int half) __attribute__((always_inline)) {
-    constexpr int G = 4 * RB;  // groups of weights, over KS steps; packed a step after they are taken
+  auto phase_scores = [&](f32x16_t& x, const f32x16_t& y, int vbuf, int half) __attribute__((always_inline)) {
+    constexpr int G = 4;  // groups of weights, over KS steps; packed a step after they are taken
     float p[2][4];
     zero(x);
 #pragma unroll
@@ -352,41 +323,30 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : kWaves / 4) void mx_atte
   // whole block of 32 elements at once.
   u32x4_t flag;  // of V[t], one word for 16 tokens
   auto read_flag = [&](int buf) __attribute__((always_inline)) {
-    flag = *(const u32x4_t*)(smem + L::FlagAt + buf * 32);
-    if constexpr (H == 2) flag |= *(const u32x4_t*)(smem + L::FlagAt + buf * 32 + 16);
+    flag = *(const u32x4_t*)(smem + L::FlagAt + buf * 16);
   };
   auto nans = [&](int buf, int tile, uint32_t there) __attribute__((always_inline)) {
     if (__builtin_amdgcn_readfirstlane(flag[0] | flag[1] | flag[2] | flag[3]) == 0) return;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       if (__builtin_amdgcn_readfirstlane(flag[k]) == 0) continue;
-      bf16x8_t seen[RB];
+      uint32_t bits = 0;
 #pragma unroll
-      for (int r = 0; r < RB; ++r) {
-        uint32_t bits = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int t = tile * kTile + 16 * k + 8 * (i >> 2) + 4 * h + (i & 3);
-          bits |= sees(r, t, there, k) ? 1u << i : 0u;
-        }
-        seen[r] = mx_ones(bits);
-      }
+      for (int i = 0; i < 8; ++i)
+        bits |= sees(tile * kTile + 16 * k + 8 * (i >> 2) + 4 * h + (i & 3), there, k) ? 1u << i : 0u;
+      const bf16x8_t seen = mx_ones(bits);
 #pragma unroll
       for (int d = 0; d < DB; ++d) {
-        uint32_t bits = 0;
+        bits = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           bits |= smem[L::NanAt + buf * L::Nan + d * kTile + 16 * k + 8 * (i >> 2) + 4 * h + (i & 3)] ? 1u << i : 0u;
-        const bf16x8_t is_nan = mx_ones(bits);
+        f32x16_t hit;
 #pragma unroll
-        for (int r = 0; r < RB; ++r) {
-          f32x16_t hit;
+        for (int i = 0; i < 16; ++i) hit[i] = 0.0f;
+        hit = __builtin_amdgcn_mfma_f32_32x32x16_bf16(mx_ones(bits), seen, hit, 0, 0, 0);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) hit[i] = 0.0f;
-          hit = __builtin_amdgcn_mfma_f32_32x32x16_bf16(is_nan, seen[r], hit, 0, 0, 0);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[r][d][i] = hit[i] > 0.0f ? NAN : o[r][d][i];
-        }
+        for (int i = 0; i < 16; ++i) o[d][i] = hit[i] > 0.0f ? NAN : o[d][i];
       }
     }
   };
@@ -478,55 +438,46 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 2 : kWaves / 4) void mx_atte
   }
 
   // ---- the rows' results: lane (n, h) has elements 32 d + 8 k + 4 h .. + 3 of row n ----
-#pragma unroll
-  for (int r = 0; r < RB; ++r) {
-    const float sum = l[r] + __shfl_xor(l[r], 32, 64);
-    const int p = p0 + r * 32 + n;
-    if (p >= rows.count) continue;
-    const int64_t token = rows.r0 + p / g;
-    const int head = kvh * g + p % g;
-    if (a.splits > 1) {
-      const int64_t at = ((int64_t)split * a.b.tokens + token) * a.heads + head;
-      if (h == 0) a.part_ml[at] = make_float2(m[r], sum);
-      if (sum != 0.0f) {
-#pragma unroll
-        for (int d = 0; d < DB; ++d)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            *(f32x4_t*)(a.part_o + at * D + 32 * d + 8 * k + 4 * h) =
-                f32x4_t{o[r][d][4 * k], o[r][d][4 * k + 1], o[r][d][4 * k + 2], o[r][d][4 * k + 3]};
-      }
-    } else {
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-      uint16_t* dst = a.out + token * a.out_token + (int64_t)head * a.out_head;
+  const float all_sum = l + __shfl_xor(l, 32, 64);
+  if (!real) return;
+  const int64_t token = rows.r0 + pn / g;
+  const int head = kvh * g + pn % g;
+  if (a.splits > 1) {
+    const int64_t at = ((int64_t)split * a.b.tokens + token) * a.heads + head;
+    if (h == 0) a.part_ml[at] = make_float2(m, all_sum);
+    if (all_sum != 0.0f) {
 #pragma unroll
       for (int d = 0; d < DB; ++d)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          *(u32x2_t*)(dst + 32 * d + 8 * k + 4 * h) =
-              u32x2_t{pack_bf16(o[r][d][4 * k] * inv, o[r][d][4 * k + 1] * inv),
-                      pack_bf16(o[r][d][4 * k + 2] * inv, o[r][d][4 * k + 3] * inv)};
+          *(f32x4_t*)(a.part_o + at * D + 32 * d + 8 * k + 4 * h) =
+              f32x4_t{o[d][4 * k], o[d][4 * k + 1], o[d][4 * k + 2], o[d][4 * k + 3]};
     }
+  } else {
+    const float inv = all_sum == 0.0f ? 0.0f : 1.0f / all_sum;
+    uint16_t* dst = a.out + token * a.out_token + (int64_t)head * a.out_head;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        *(u32x2_t*)(dst + 32 * d + 8 * k + 4 * h) =
+            u32x2_t{pack_bf16(o[d][4 * k] * inv, o[d][4 * k + 1] * inv),
+                    pack_bf16(o[d][4 * k + 2] * inv, o[d][4 * k + 3] * inv)};
   }
 }
 
 template <int D>
-struct Form {
-  static constexpr int RB = D == 64 ? 2 : 1, W = D == 128 ? 8 : 4;
-};
-
-template <int D, int RB = Form<D>::RB, int W = Form<D>::W>
 hipError_t launch_prompt(const MxAttnArgs& a, hipStream_t stream) {
-  const int64_t tiles = a.b.tokens * a.group / (32 * RB * W) + a.b.batch;
-  mx_attention_prompt_kernel<D, RB, W>
-      <<<dim3((unsigned)(tiles * a.c.kv_heads), a.splits), 64 * W, Lds<D>::Bytes, stream>>>(a);
+  const int64_t tiles = a.b.tokens * a.group / kRows + a.b.batch;
+  mx_attention_prompt_kernel<D>
+      <<<dim3((unsigned)(tiles * a.c.kv_heads), a.splits), 64 * kWaves, Lds<D>::Bytes, stream>>>(a);
   return hipGetLastError();
 }
 
-template <int D, int RB = Form<D>::RB, int W = Form<D>::W>
+template <int D>
 hipError_t setup_prompt() {
-  return hipFuncSetAttribute((const void*)mx_attention_prompt_kernel<D, RB, W>,
-                             hipFuncAttributeMaxDynamicSharedMemorySize, Lds<D>::Bytes);
+  return hipFuncSetAttribute((const void*)mx_attention_prompt_kernel<D>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                             Lds<D>::Bytes);
 }
 
 }  // namespace

@@ -329,3 +329,48 @@ def test_refusals(gpu):
         nv.mxfp4_cache_append(c.cache, x[:, :1], x, c.table, c.seq, c.cu)
     with pytest.raises(nv.Nvfp4Error):
         nv.mxfp4_cache_read(*good, 2, out=(x[:1].expand(2, -1, -1), x))
+
+
+@pytest.mark.parametrize("call", [{}, dict(window=700, sinks=70), dict(causal=False)])
+@pytest.mark.parametrize("kw,lens", [(dict(group=2), [(40, 1500), (33, 80)]), (dict(group=3, kv_heads=1, dim=64), [(50, 1300)]),
+                                     (dict(group=1, dim=256, page=32), [(70, 1100), (3, 0), (40, 500)])])
+def test_prompts_in_pieces(gpu, kw, lens, call):
+    """More rows than the few-rows form takes, over a cache that is split."""
+    import nvfp4_block_scaled_swiglu_amd as nv
+    c = Case(gpu, lens, **kw).fill(gpu)
+    args = (c.cache, c.table, c.seq, c.cu)
+    assert nv.mxfp4_attention_workspace_bytes(*args, c.tokens, c.heads, 1 << 14) > 0
+    c.check(nv.mxfp4_attention(c.q, *args, max_kv=1 << 14, **call), **call)
+
+
+@pytest.mark.parametrize("q", [1, 90])
+def test_bounds_that_bound_nothing(gpu, q):
+    """The largest max_kv, window and sinks are those of no limit."""
+    import torch
+    import nvfp4_block_scaled_swiglu_amd as nv
+    c = Case(gpu, [(q, 300), (q, 91)], group=2).fill(gpu)
+    args = (c.q, c.cache, c.table, c.seq, c.cu)
+    most = 2 ** 63 - 1
+    for kw in (dict(max_kv=most), dict(max_kv=most, window=most, sinks=most), dict(window=most), dict(window=1, sinks=most)):
+        c.check(nv.mxfp4_attention(*args, **kw))
+
+
+@pytest.mark.parametrize("q", [1, 40])
+def test_pages_of_two_sequences(gpu, q):
+    """Sequences that share the pages of a common beginning, a table that is a slice of a wider
+    one, and the queries' own memory as output."""
+    import torch
+    import nvfp4_block_scaled_swiglu_amd as nv
+    c = Case(gpu, [(q, 160), (q, 160)], group=2).fill(gpu)
+    wide = torch.full((2, c.table.shape[1] + 3), -1, dtype=torch.int32, device=gpu)
+    wide[:, 2:2 + c.table.shape[1]] = c.table
+    wide[1, 2:8] = wide[0, 2:8]  # tokens 0 .. 95 of the first
+    half = c.k_bits.shape[0] // 2
+    for bits in (c.k_bits, c.v_bits):
+        bits[half:half + 96] = bits[:96]
+    table = wide[:, 2:2 + c.table.shape[1]]
+    own = c.q.clone()
+    for kv in (160, 1 << 14):
+        c.check(nv.mxfp4_attention(c.q, c.cache, table, c.seq, c.cu, max_kv=kv))
+    assert nv.mxfp4_attention(own, c.cache, table, c.seq, c.cu, out=own) is own
+    c.check(own)
