@@ -37,6 +37,8 @@
 // The maximum is raised only when a score exceeds it by more than 2^8: until then weights
 // up to 2^8 are as exact as those below 1, and most tiles skip the cross-lane maximum and
 // the rescaling of O.
+#include <type_traits>
+
 #include "mx_attn.hpp"
 
 namespace nvfp4 {
@@ -47,7 +49,6 @@ constexpr int kWaves = 4;
 constexpr int kTile = 32;  // tokens per step
 
 typedef __attribute__((address_space(3))) void lds_ptr_t;
-typedef const __attribute__((address_space(1))) void global_ptr_t;
 
 // A ring slot: K codes, V codes, K scales, V scales of 32 tokens, in the cache's order.
 template <int D>
@@ -55,9 +56,8 @@ struct Slot {
   static constexpr int Codes = kTile * D / 2, Half = Codes / 2;   // bytes; Half: of 16 tokens
   static constexpr int Scales = kTile * D / 32, SHalf = Scales / 2;
   static constexpr int V = Codes, KS = 2 * Codes, VS = KS + Scales, Bytes = VS + Scales;
-  static constexpr int CodeLoads = Codes / 1024;                  // 16 bytes a lane, of K and of V
-  static constexpr int ScaleLoads = (2 * Scales + 255) / 256;     // a dword a lane, of both
-  static constexpr int Loads = 2 * CodeLoads + ScaleLoads;
+  // instructions for a run of tokens: 16 bytes a lane of codes, 4 of scales
+  static constexpr int loads(int tokens) { return 2 * ((tokens * D / 2 + 1023) / 1024 + (tokens * D / 32 + 255) / 256); }
 };
 
 // Workgroups of a CU, by registers, and the ring slots of a wave that then fit: 34 KiB for a
@@ -66,6 +66,15 @@ struct Slot {
 // more waves hide more than more slots.
 constexpr int groups_per_cu(int d, int rt) { return d * rt <= 128 ? (rt == 1 ? 4 : 3) : d * rt <= 256 ? 2 : 1; }
 constexpr int ring_slots(int d, int rt) { return (d * rt <= 128 ? 256 : 512) / d; }
+
+// LDS of a workgroup: the rings, where the waves' outputs meet afterwards, and their maxima and
+// sums. (Dynamic: of static LDS the compiler knows which object a load into it writes, and
+// waits for all loads in flight before any read of that object.)
+template <int D, int RT>
+struct FewLds {
+  static constexpr int Rings = kWaves * ring_slots(D, RT) * Slot<D>::Bytes, Red = kWaves * (D / 4) * 64 * 4;
+  static constexpr int Ring = Rings > Red ? Rings : Red, Bytes = Ring + 2 * kWaves * RT * 16 * 4;
+};
 
 template <int N>
 __device__ __forceinline__ void wait_loads() {  // vmcnt(N)
@@ -79,10 +88,8 @@ __global__ __launch_bounds__(64 * kWaves, groups_per_cu(D, RT)) void mx_attentio
   using S = Slot<D>;
   constexpr int NJ = D / 16, KS = D / 32, E = D / 4, R = ring_slots(D, RT);
   constexpr int kRows = 16 * RT;  // packed rows of the workgroup
-  constexpr int kRed = kWaves * E * 64 * 4;
-  constexpr int kLds = kWaves * R * S::Bytes > kRed ? kWaves * R * S::Bytes : kRed;
-  __shared__ __align__(16) uint8_t smem[kLds];
-  __shared__ float ml[2 * kWaves * RT * 16];
+  extern __shared__ __align__(16) uint8_t smem[];
+  float* const ml = (float*)(smem + FewLds<D, RT>::Ring);
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -117,7 +124,7 @@ __global__ __launch_bounds__(64 * kWaves, groups_per_cu(D, RT)) void mx_attentio
   const MxSight sight = mx_sight(a, rows, p0, p1);
   const int high_min = p1 - p0 < kRows ? 0 : sight.high_min;  // rows that are not there see nothing
   const MxSpan span = mx_span(sight, kTile);
-  const int from = (int)((int64_t)span.count * split / a.splits), to = (int)((int64_t)span.count * (split + 1) / a.splits);
+  const int from = mx_share(span.count, split, a.splits), to = mx_share(span.count, split + 1, a.splits);
   const int begin = from + (to - from) * wave / kWaves, end = from + (to - from) * (wave + 1) / kWaves;
 
   // ---- loads ----
@@ -135,6 +142,7 @@ __global__ __launch_bounds__(64 * kWaves, groups_per_cu(D, RT)) void mx_attentio
     return __builtin_amdgcn_readlane(entry, p - base);
   };
   uint8_t* const ring = smem + wave * (R * S::Bytes);
+  const bool halves = a.b.page_shift == 4;  // else the halves of a tile share a page
   uint32_t there_bits = 0;  // bits 2 slot, 2 slot + 1: the page of each 16-token half exists
   auto load = [&](int slot, int tile) __attribute__((always_inline)) {
     const int t0 = tile * kTile;
@@ -143,31 +151,41 @@ __global__ __launch_bounds__(64 * kWaves, groups_per_cu(D, RT)) void mx_attentio
     uint32_t there = page >= 0 ? 3u : 0u;
     row[0] = mx_cache_row(a, page, kvh, t0);
     row[1] = row[0] + 16;
-    if (a.b.page_shift == 4) {  // else the halves share a page
+    if (halves) {
       page = t0 + 16 < rows.kv_len ? page_of(t0 + 16) : -1;
       there = (there & 1u) | (page >= 0 ? 2u : 0u);
       row[1] = mx_cache_row(a, page, kvh, t0 + 16);
     }
     there_bits = (there_bits & ~(3u << (2 * slot))) | (there << (2 * slot));
     uint8_t* dst = ring + slot * S::Bytes;
+    // (buffer loads: behind global loads into LDS the compiler would wait for all of them
+    // at each of the step's reads)
+    auto move_all = [&](int64_t row, int token, auto tokens) __attribute__((always_inline)) {
+      constexpr int kCodes = decltype(tokens)::value * D / 2, kScales = decltype(tokens)::value * D / 32;
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      const uint8_t* codes = kv ? a.c.v_codes : a.c.k_codes;
+      for (int kv = 0; kv < 2; ++kv) {
+        const __amdgpu_buffer_rsrc_t from = __builtin_amdgcn_make_buffer_rsrc(
+            (kv ? a.c.v_codes : a.c.k_codes) + row * (D / 2), 0, kCodes, 0x00020000);
+        uint8_t* to = dst + (kv ? S::V : 0) + token * (D / 2);
 #pragma unroll
-      for (int j = 0; j < S::CodeLoads; ++j) {
-        const int at = j * 1024 + lane * 16, h = at / S::Half;
-        const uint8_t* src = codes + (h ? row[1] : row[0]) * (D / 2) + (at - h * S::Half);
-        __builtin_amdgcn_global_load_lds((global_ptr_t*)src, (lds_ptr_t*)(dst + kv * S::V + j * 1024), 16, 0, 0);
+        for (int at = 0; at < kCodes; at += 1024)
+          if (kCodes - at >= 1024 || lane * 16 < kCodes - at)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_ptr_t*)(to + at), 16, at + lane * 16, 0, 0, 0);
       }
-    }
 #pragma unroll
-    for (int j = 0; j < S::ScaleLoads; ++j) {
-      const int at = j * 256 + lane * 4;
-      const int which = at / S::SHalf;  // K half 0, 1, V half 0, 1
-      const uint8_t* src = (which >= 2 ? a.c.v_scales : a.c.k_scales) + ((which & 1) ? row[1] : row[0]) * (D / 32) +
-                           (at - which * S::SHalf);
-      if (at < 2 * S::Scales)
-        __builtin_amdgcn_global_load_lds((global_ptr_t*)src, (lds_ptr_t*)(dst + S::KS + j * 256), 4, 0, 0);
+      for (int kv = 0; kv < 2; ++kv) {
+        const __amdgpu_buffer_rsrc_t from = __builtin_amdgcn_make_buffer_rsrc(
+            (kv ? a.c.v_scales : a.c.k_scales) + row * (D / 32), 0, kScales, 0x00020000);
+        if (lane * 4 < kScales)
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_ptr_t*)(dst + (kv ? S::VS : S::KS) + token * (D / 32)), 4,
+                                                   lane * 4, 0, 0, 0);
+      }
+    };
+    if (halves) {
+      move_all(row[0], 0, std::integral_constant<int, 16>());
+      move_all(row[1], 16, std::integral_constant<int, 16>());
+    } else {
+      move_all(row[0], 0, std::integral_constant<int, kTile>());
     }
   };
 
@@ -316,11 +334,14 @@ __global__ __launch_bounds__(64 * kWaves, groups_per_cu(D, RT)) void mx_attentio
   // count of loads in flight stays what the waits assume. A slot is refilled once its reads
   // have returned (lgkmcnt(0)).
   if (begin < end) {
+    page_of(span.at(begin) * kTile);
+    wait_loads<0>();  // the rows are here: no step waits for them, and with them for the ring
 #pragma unroll
     for (int i = 0; i < R; ++i) load(i, span.at(begin + i < end ? begin + i : end - 1));
     int slot = 0;
     for (int i = begin; i < end; ++i) {
-      wait_loads<(R - 1) * S::Loads>();
+      if (halves) wait_loads<(R - 1) * S::loads(16) * 2>();
+      else wait_loads<(R - 1) * S::loads(32)>();
       step(slot, span.at(i));
       asm volatile("" ::: "memory");
       __builtin_amdgcn_s_waitcnt(0xC07F);
@@ -408,9 +429,7 @@ __global__ __launch_bounds__(256) void mx_attention_join_kernel(MxAttnArgs a) {
   const int64_t pair = blockIdx.x, pairs = a.b.tokens * a.heads;
   const int64_t token = pair / a.heads;
   const int head = (int)(pair - token * a.heads);
-  int pos;
-  int64_t page;
-  if (!mx_locate(a.b, token, pos, page)) return;  // a row of no sequence stays as it was
+  if (token < mx_row_start(a.b, 0) || token >= mx_row_start(a.b, a.b.batch)) return;  // of no sequence: stays as it was
   float2 v = make_float2(-INFINITY, 0.0f);
   if (tid < a.splits) v = a.part_ml[tid * pairs + pair];
   if (v.y == 0.0f) v.x = -INFINITY;  // saw nothing; its o was not written
@@ -453,7 +472,7 @@ __global__ __launch_bounds__(256) void mx_attention_join_kernel(MxAttnArgs a) {
 template <int D, int RT>
 hipError_t launch_few(const MxAttnArgs& a, hipStream_t stream) {
   const int64_t tiles = a.b.tokens * a.group / (16 * RT) + a.b.batch;
-  mx_attention_few_kernel<D, RT><<<dim3((unsigned)(tiles * a.c.kv_heads), a.splits), 64 * kWaves, 0, stream>>>(a);
+  mx_attention_few_kernel<D, RT><<<dim3((unsigned)(tiles * a.c.kv_heads), a.splits), 64 * kWaves, FewLds<D, RT>::Bytes, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -469,7 +488,29 @@ hipError_t launch_dim(const MxAttnArgs& a, const MxAttnPlan& plan, hipStream_t s
   return hipGetLastError();
 }
 
+template <int D, int RT>
+hipError_t setup_few() {
+  return hipFuncSetAttribute((const void*)mx_attention_few_kernel<D, RT>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                             FewLds<D, RT>::Bytes);
+}
+
+template <int D>
+hipError_t setup_dim() {
+  hipError_t e = setup_few<D, 1>();
+  if (e == hipSuccess) e = setup_few<D, 2>();
+  if (e == hipSuccess && D != 256) e = setup_few<D, D == 256 ? 2 : 4>();
+  return e;
+}
+
 }  // namespace
+
+hipError_t mx_attention_setup() {
+  hipError_t e = setup_dim<64>();
+  if (e == hipSuccess) e = setup_dim<128>();
+  if (e == hipSuccess) e = setup_dim<256>();
+  if (e == hipSuccess) e = mx_attention_prompt_setup();
+  return e;
+}
 
 hipError_t launch_mx_attention(const MxAttnArgs& a, const MxAttnPlan& plan, hipStream_t stream) {
   switch (a.c.head_dim) {

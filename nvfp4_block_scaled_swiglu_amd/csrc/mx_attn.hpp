@@ -77,6 +77,7 @@ inline MxAttnPlan mx_attention_plan(int64_t tokens, int64_t batch, int64_t heads
   return p;
 }
 
+hipError_t mx_attention_prompt_setup();
 hipError_t launch_mx_attention_prompt(const MxAttnArgs& a, hipStream_t stream);
 
 // ---- device side ----
@@ -211,6 +212,13 @@ __device__ __forceinline__ MxSpan mx_span(const MxSight& s, int size) {
   const int end = (s.high_max + size - 1) / size;
   t.count = t.first + (end > t.begin ? end - t.begin : 0);
   return t;
+}
+
+// where share i of n shares of a count begins, the first ones larger by one if need be
+// (count * i / n needs a 64-bit division, 200 instructions before the first load)
+__device__ __forceinline__ int mx_share(int count, int i, int n) {
+  const int each = (int)((unsigned)count / (unsigned)n), over = count - each * n;
+  return each * i + (i < over ? i : over);
 }
 
 // the page of token t of sequence seq, or -1

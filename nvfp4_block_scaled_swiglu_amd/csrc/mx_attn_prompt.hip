@@ -88,8 +88,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D)) void mx_attention_p
   const int wg_end = rows.first + kRows < rows.count ? rows.first + kRows : rows.count;
   const MxSight all = mx_sight(a, rows, rows.first, wg_end);
   const MxSpan span = mx_span(all, kTile);
-  const int begin = (int)((int64_t)span.count * split / a.splits);
-  const int end = (int)((int64_t)span.count * (split + 1) / a.splits);
+  const int begin = mx_share(span.count, split, a.splits), end = mx_share(span.count, split + 1, a.splits);
 
   // ---- the wave's rows ----
   const int p0 = rows.first + wave * 32;
@@ -482,7 +481,7 @@ hipError_t setup_prompt() {
 
 }  // namespace
 
-hipError_t mx_attention_setup() {
+hipError_t mx_attention_prompt_setup() {
   hipError_t e = setup_prompt<64>();
   if (e == hipSuccess) e = setup_prompt<128>();
   if (e == hipSuccess) e = setup_prompt<256>();
