@@ -169,7 +169,8 @@ int64_t mxfp4_attention_workspace_bytes(const mxfp4_cache* cache, const mxfp4_ba
  *                  be NULL if that is 0. Its contents before and after mean nothing. Calls
  *                  that may overlap in time need distinct workspaces.
  * Scores, the softmax and its sums are fp32; weights are rounded to bf16 for their product
- * with the values, and so for their sum. The order of every sum depends on the arguments and lengths alone.
+ * with the values, and so for their sum. The order of every sum depends on the arguments and
+ * lengths alone.
  */
 int mxfp4_attention(const mxfp4_cache* cache, const mxfp4_batch* batch, const void* q_dev, int64_t q_token_stride,
                     int64_t q_head_stride, int64_t heads, float scale, int causal, int64_t window, int64_t sinks,

@@ -11,9 +11,10 @@
 //
 // What bounds it is reading the cache: every visible token once per kv head, 17/32 bytes an
 // element. A wave moves its codes and scales to a ring of its own in LDS, 32 tokens a slot,
-// with direct-to-LDS loads that need no register while they fly and no barrier (five
+// with direct-to-LDS loads that need no register while they fly and no barrier (six
 // instructions for 32 tokens of 128 elements, every one of whole runs): 16 waves x 2 slots
-// x 4.25 KiB in flight per CU.
+// x 4.25 KiB in flight per CU. 48 single tokens over up to 8200, 56 heads of 128 over 8: 78
+// us and 7 of joining, 4.2 TB/s of the cache; the loads alone take 63, the rest alone 69.
 //
 // One pass with the running maximum and sum of the softmax, in the transposed form with
 // v_mfma_f32_16x16x32_bf16, lane (n, u) = (lane & 15, lane >> 4):
@@ -60,19 +61,18 @@ struct Slot {
   static constexpr int loads(int tokens) { return 2 * ((tokens * D / 2 + 1023) / 1024 + (tokens * D / 32 + 255) / 256); }
 };
 
-// Workgroups of a CU, by registers, and the ring slots of a wave that then fit: 34 KiB for a
-// workgroup of four waves, or 68 KiB. Measured on 48 single tokens over up to 8200 (D 128,
-// RT 1): four workgroups with 2 slots 92 us, three with 3 slots 103, two with 4 slots 120 -
-// more waves hide more than more slots.
-constexpr int groups_per_cu(int d, int rt) { return d * rt <= 128 ? (rt == 1 ? 4 : 3) : d * rt <= 256 ? 2 : 1; }
-constexpr int ring_slots(int d, int rt) { return (d * rt <= 128 ? 256 : 512) / d; }
+// Workgroups of a CU, by registers, and the ring slots of a wave that then fit. Measured on 48
+// single tokens over up to 8200 of 128: four workgroups with 2 slots 85 us, three with 2 the
+// same, three with 3 slots 91 - more waves hide more than more slots.
+constexpr int groups_per_cu(int d, int rt) { return d == 256 ? 2 : rt == 1 ? 4 : 3; }
+constexpr int ring_slots(int d) { return d == 64 ? 4 : 2; }
 
 // LDS of a workgroup: the rings, where the waves' outputs meet afterwards, and their maxima and
 // sums. (Dynamic: of static LDS the compiler knows which object a load into it writes, and
 // waits for all loads in flight before any read of that object.)
 template <int D, int RT>
 struct FewLds {
-  static constexpr int Rings = kWaves * ring_slots(D, RT) * Slot<D>::Bytes, Red = kWaves * (D / 4) * 64 * 4;
+  static constexpr int Rings = kWaves * ring_slots(D) * Slot<D>::Bytes, Red = kWaves * (D / 4) * 64 * 4;
   static constexpr int Ring = Rings > Red ? Rings : Red, Bytes = Ring + 2 * kWaves * RT * 16 * 4;
 };
 
@@ -86,7 +86,7 @@ __device__ __forceinline__ void wait_loads() {  // vmcnt(N)
 template <int D, int RT>
 __global__ __launch_bounds__(64 * kWaves, groups_per_cu(D, RT)) void mx_attention_few_kernel(MxAttnArgs a) {
   using S = Slot<D>;
-  constexpr int NJ = D / 16, KS = D / 32, E = D / 4, R = ring_slots(D, RT);
+  constexpr int NJ = D / 16, KS = D / 32, E = D / 4, R = ring_slots(D);
   constexpr int kRows = 16 * RT;  // packed rows of the workgroup
   extern __shared__ __align__(16) uint8_t smem[];
   float* const ml = (float*)(smem + FewLds<D, RT>::Ring);
@@ -330,6 +330,7 @@ __global__ __launch_bounds__(64 * kWaves, groups_per_cu(D, RT)) void mx_attentio
   };
 
   // ---- the walk ----
+  static_assert((R - 1) * 2 * S::loads(16) <= 63, "vmcnt");
   // Slots are filled R tiles ahead; past the end the last tile is loaded again, so that the
   // count of loads in flight stays what the waits assume. A slot is refilled once its reads
   // have returned (lgkmcnt(0)).
@@ -472,7 +473,8 @@ __global__ __launch_bounds__(256) void mx_attention_join_kernel(MxAttnArgs a) {
 template <int D, int RT>
 hipError_t launch_few(const MxAttnArgs& a, hipStream_t stream) {
   const int64_t tiles = a.b.tokens * a.group / (16 * RT) + a.b.batch;
-  mx_attention_few_kernel<D, RT><<<dim3((unsigned)(tiles * a.c.kv_heads), a.splits), 64 * kWaves, FewLds<D, RT>::Bytes, stream>>>(a);
+  mx_attention_few_kernel<D, RT>
+      <<<dim3((unsigned)(tiles * a.c.kv_heads), a.splits), 64 * kWaves, FewLds<D, RT>::Bytes, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -481,8 +483,7 @@ hipError_t launch_dim(const MxAttnArgs& a, const MxAttnPlan& plan, hipStream_t s
   hipError_t e;
   if (!plan.few) e = launch_mx_attention_prompt(a, stream);
   else if (plan.row_tiles == 1) e = launch_few<D, 1>(a, stream);
-  else if (plan.row_tiles == 2) e = launch_few<D, 2>(a, stream);
-  else e = launch_few<D, D == 256 ? 2 : 4>(a, stream);
+  else e = launch_few<D, D == 64 ? 2 : 1>(a, stream);  // two: only of 64
   if (e != hipSuccess || a.splits == 1) return e;
   mx_attention_join_kernel<D><<<(unsigned)(a.b.tokens * a.heads), 256, 0, stream>>>(a);
   return hipGetLastError();
@@ -494,20 +495,13 @@ hipError_t setup_few() {
                              FewLds<D, RT>::Bytes);
 }
 
-template <int D>
-hipError_t setup_dim() {
-  hipError_t e = setup_few<D, 1>();
-  if (e == hipSuccess) e = setup_few<D, 2>();
-  if (e == hipSuccess && D != 256) e = setup_few<D, D == 256 ? 2 : 4>();
-  return e;
-}
-
 }  // namespace
 
 hipError_t mx_attention_setup() {
-  hipError_t e = setup_dim<64>();
-  if (e == hipSuccess) e = setup_dim<128>();
-  if (e == hipSuccess) e = setup_dim<256>();
+  hipError_t e = setup_few<64, 1>();
+  if (e == hipSuccess) e = setup_few<64, 2>();
+  if (e == hipSuccess) e = setup_few<128, 1>();
+  if (e == hipSuccess) e = setup_few<256, 1>();
   if (e == hipSuccess) e = mx_attention_prompt_setup();
   return e;
 }

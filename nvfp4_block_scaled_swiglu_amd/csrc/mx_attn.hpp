@@ -28,13 +28,16 @@ struct MxAttnPlan {
   int splits;     // pieces of the token axis, joined by a second launch
 };
 
-// Rows: the packed rows (rows x heads of a group) of an average sequence. Up to 64 of them
-// (32 at head_dim 256) are one workgroup's of the few-rows form, whose four waves split the
-// tokens; beyond that the prompt form gives every wave 32 rows of its own.
+// Rows: the packed rows (rows x heads of a group) of an average sequence. Up to 16 of them
+// (32 at head_dim 64) are one workgroup's of the few-rows form, whose four waves split the
+// tokens; beyond that the prompt form gives every wave 32 rows of its own. Measured, 64
+// sequences of 2048, 8 kv heads, few-rows form and prompt form: 16 rows of 128 65 and 96 us,
+// 32 rows 118 and 94; of 64, 32 rows 80 and 97, 48 rows 110 and 97; of 256, 16 rows 127 and
+// 233, 32 rows 251 and 225.
 //
 // Splits: where the rows alone do not give enough workgroups, pieces of the token axis do.
 // Few rows: 8 workgroups for each of the 256 CUs (ragged lengths then even out over two
-// rounds of them: 48 tokens over up to 8200 take 92 us with 5 splits, 108 with 2, 97 with 8),
+// rounds of them: 48 tokens over up to 8200 take 80 us with 5 splits, 94 with 2, 86 with 10),
 // but at least two 32-token tiles a wave, so that a split is more than its own start.
 // Prompts: as many as are resident at once, by registers 3, 2 or 1 a CU. But a split writes
 // and reads every row once more in fp32, head_dim tokens heads splits * 4 ps as measured,
@@ -49,9 +52,8 @@ inline MxAttnPlan mx_attention_plan(int64_t tokens, int64_t batch, int64_t heads
   if (tokens <= 0 || batch <= 0) return p;
   const int64_t group = heads / kv_heads;
   const int64_t rows = (tokens + batch - 1) / batch * group;
-  const int most = head_dim == 256 ? 2 : 4;
-  p.few = rows <= 16 * most;
-  p.row_tiles = rows <= 16 ? 1 : rows <= 32 ? 2 : most;
+  p.row_tiles = rows <= 16 ? 1 : 2;
+  p.few = p.row_tiles == 1 || (head_dim == 64 && rows <= 32);
   const int64_t per_group = p.few ? 16 * p.row_tiles : 128;
   int64_t tiles = (tokens * group + per_group - 1) / per_group;
   if (tiles < batch) tiles = batch;
