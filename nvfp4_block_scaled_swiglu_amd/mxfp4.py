@@ -136,9 +136,9 @@ def _bf16(t, name: str, dim: int, shape=None):
     import torch
     if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.dim() != dim or not t.is_cuda:
         raise ValueError(f"{name} must be a {dim}-D bfloat16 CUDA tensor")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name} must have unit stride in its last dimension")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     return t
 
@@ -168,7 +168,7 @@ def _int32(t, name: str, dim: int):
     import torch
     if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != dim or not t.is_cuda:
         raise ValueError(f"{name} must be a {dim}-D int32 CUDA tensor")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name} must have unit stride in its last dimension")
     return t
 
@@ -346,9 +346,9 @@ def mxfp4_cache_append(cache: Mxfp4Cache, k, v, block_table, seq_lens, cu_seqlen
     """Quantize new keys and values (bf16 [tokens, kv_heads, head_dim]) into the cache at their
     rows' positions, the last ones of each sequence. Returns the cache."""
     c, ct = _cache(cache)
-    _bf16(k, "k", 3)
-    shape = (k.shape[0], c.kv_heads, c.head_dim)
-    _bf16(k, "k", 3, shape)
+    shape = _bf16(k, "k", 3).shape
+    if shape[1] != c.kv_heads or shape[2] != c.head_dim:
+        raise ValueError(f"k must have shape {(shape[0], c.kv_heads, c.head_dim)}, not {tuple(shape)}")
     _bf16(v, "v", 3, shape)
     b, bt = _batch(block_table, seq_lens, cu_seqlens, shape[0])
     with _On(stream, k, v, *ct, *bt) as on:
