@@ -223,13 +223,6 @@ __device__ __forceinline__ int mx_share(int count, int i, int n) {
   return each * i + (i < over ? i : over);
 }
 
-// the page of token t of sequence seq, or -1
-__device__ __forceinline__ int64_t mx_page(const MxAttnArgs& a, const MxRows& r, int t) {
-  if (t >= r.kv_len) return -1;
-  const int64_t p = a.b.block_table[(int64_t)r.seq * a.b.table_stride + (t >> a.b.page_shift)];
-  return p >= 0 && p < a.b.num_pages ? p : -1;
-}
-
 // first of the cache's rows for 16 tokens from t (a multiple of 16) on that page; a page
 // that is not there is read as page 0, and what is read must not be used
 __device__ __forceinline__ int64_t mx_cache_row(const MxAttnArgs& a, int64_t page, int head, int t) {
