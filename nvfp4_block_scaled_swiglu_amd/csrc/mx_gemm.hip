@@ -7,6 +7,8 @@
 // each lane giving the 16 code bytes and one scale byte of its (row, block). Every product
 // is exact and the sums are fp32. The rate is four times that of fp16, so a K step has a
 // quarter of the time to bring its operands that the fp16 form has per element.
+#include <type_traits>
+
 #include "mx.hpp"
 
 namespace nvfp4 {
@@ -42,41 +44,43 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 // ---- tiles ---------------------------------------------------------------------------------
-// A workgroup of 4 waves (2 x 2) computes (64 FM) x (64 FN), FM = FN = 4 for whole tiles; a wave owns FM x FN tiles of
-// 32 x 32. K advances 128 per step: 64 code bytes a row and one 512-byte scale tile per
-// 128 rows. Direct-to-LDS loads bring step ks + kStages while step ks is multiplied.
-// A step has two halves of one MFMA per tile each: while the MFMAs of a half run, the
+// A workgroup of 4 waves (2 x 2) computes (64 FM) x (64 FN), FM = FN = 4 for whole tiles; a
+// wave owns FM x FN tiles of 32 x 32. A stage in LDS holds two K steps of 128: 128 code bytes
+// a row, which a load instruction takes whole from 8 rows, and a KiB of scales per 128 rows.
+// (64 bytes from 16 rows fetch every line twice: 37810 x 5376 x 14336 1,405 us instead of
+// 1,370, 1536 x 5376 x 14336 70.8 instead of 63.5.) Direct-to-LDS loads bring pair ps + kStages while pair
+// ps is multiplied.
+// A pair has four quarters of one MFMA per tile each: while the MFMAs of a quarter run, the
 // fragments of the next are read from LDS, in a fixed order of fenced steps (left alone they
 // gather in front of the MFMAs that use them, and one wave a SIMD waits for each). The
-// barrier sits between the halves: every wave has then read both halves of step ks, whose
-// stage takes the loads of step ks + kStages, in the second half of this step and the first
-// of the next; and each has seen its own loads of step ks + 1 land.
+// barrier sits before the last quarter: every wave has then read all of the pair, whose
+// stage takes the loads of pair ps + kStages, in this quarter and the first of the next pair;
+// and each has seen its own loads of pair ps + 1 land.
 constexpr int kWaves = 4;
 constexpr int kBand = 8;  // M tiles per traversal band
 constexpr int kCus = 256, kEdge = 256;
 
 template <int FM, int FN>
 struct Shape {
-  static constexpr int kStages = FM * FN >= 8 ? 3 : 4;  // one more changes nothing
+  static constexpr int kStages = FM * FN == 16 ? 2 : 3;  // a quarter with 2: 19.6 for 16.5 us, with 4 the same
   static constexpr int TM = 64 * FM, TN = 64 * FN;
-  static constexpr int CodesA = TM * 64, CodesW = TN * 64;
-  static constexpr int ScaleA = TM / 128 * 512, ScaleW = TN / 128 * 512;
-  static constexpr int Stage = CodesA + CodesW + ScaleA + ScaleW;
+  static constexpr int CodesA = TM * 128, CodesW = TN * 128;
+  static constexpr int TilesA = TM / 128, Tiles = TilesA + TN / 128;   // of 128 rows of scales, 1 KiB each
+  static constexpr int Stage = CodesA + CodesW + Tiles * 1024;
   static constexpr int LoadsA = CodesA / 1024 / kWaves, LoadsW = CodesW / 1024 / kWaves;
-  static constexpr int Pieces = (ScaleA + ScaleW) / 256;            // scale loads: a dword a lane
-  static constexpr int LoadsS = (Pieces + kWaves - 1) / kWaves;
-  static constexpr int Loads = LoadsA + LoadsW + LoadsS;
+  static constexpr int Loads = LoadsA + LoadsW + 1;                 // the waves share the scale tiles
   static constexpr int RowBytes = 32 * FN * 2 + 16;                 // epilogue staging, padded
   static constexpr int Staging = kWaves * 32 * RowBytes;
   static constexpr int Lds = kStages * Stage > Staging ? kStages * Stage : Staging;
   static_assert(CodesA % (1024 * kWaves) == 0 && CodesW % (1024 * kWaves) == 0, "even code loads");
-  static_assert((kStages - 2) * Loads < 64, "vmcnt immediate");
+  static_assert((kStages - 1) * Loads < 64, "vmcnt immediate");
+  static_assert(Tiles <= kWaves, "scale loads");
   static_assert((FM == 4 || FM == 2) && (FN == 4 || FN == 2), "scale reads");
 };
 
-// where 16-byte chunk c of row r lies in the row's 64 LDS bytes: fragment reads (32 rows,
-// one chunk) then meet every bank
-__device__ __forceinline__ int chunk_at(int r, int c) { return c ^ (((r >> 1) ^ (r >> 2)) & 3); }
+// where 16-byte chunk c of row r lies in the row's 128 LDS bytes: the 16 rows that a phase of
+// a fragment read meets (one chunk) then lie in different banks
+__device__ __forceinline__ int chunk_at(int r, int c) { return c ^ ((r >> 1) & 7); }
 
 __device__ __forceinline__ void barrier() {
   asm volatile("" ::: "memory");
@@ -100,7 +104,7 @@ __device__ __forceinline__ void run_tile(const MxGemmArgs& a, int64_t m0, int64_
   const int wm = wave >> 1, wn = wave & 1;
   const int lr = lane & 31, h = lane >> 5;
 
-  // Buffers of the tile's own rows: reads past them return zero (codes 0 under scale 0).
+  // Buffers of the tile's own rows: reads past them return zero.
   const int krow = (int)(a.k >> 1);
   const int rows_a = (int)(a.m - m0 < T::TM ? a.m - m0 : T::TM), rows_w = (int)(a.n - n0 < T::TN ? a.n - n0 : T::TN);
   const int srow = a.groups * 512;
@@ -113,48 +117,47 @@ __device__ __forceinline__ void run_tile(const MxGemmArgs& a, int64_t m0, int64_
   __amdgpu_buffer_rsrc_t rSW = __builtin_amdgcn_make_buffer_rsrc(
       (void*)(a.ws + (n0 >> 7) * srow), 0, ((rows_w + 127) >> 7) * srow, 0x00020000);
 
-  // Load idx of this wave's share of step ks. Code load j covers rows 16 j .. 16 j + 15;
-  // lane L writes LDS bytes 16 L .. of that KiB, which hold chunk chunk_at(row, L & 3) (an
-  // involution) of row 16 j + L / 4. Chunks past K (and whole steps past the last) read
-  // past the buffer, where there is nothing but zeros.
-  auto issue = [&](int ks, int stage, int idx) __attribute__((always_inline)) {
+  // Load idx of this wave's share of pair ps. Code load j covers rows 8 j .. 8 j + 7; lane L
+  // writes LDS bytes 16 L .. of that KiB, which hold chunk chunk_at(row, L & 7) (an
+  // involution) of row 8 j + L / 8, or of the tile's last row behind it (results that are not
+  // stored; cheaper than zeros). Chunks past K (and whole pairs past the last) read past the
+  // buffer, where there is nothing but zeros.
+  auto issue = [&](int ps, int stage, int idx) __attribute__((always_inline)) {
     uint8_t* st = smem + stage * T::Stage;
     if (idx < T::LoadsA + T::LoadsW) {
       const bool is_a = idx < T::LoadsA;
       const int j = wave + (is_a ? idx : idx - T::LoadsA) * kWaves;
-      const int row = j * 16 + (lane >> 2);
-      const int c = chunk_at(row, lane & 3);
-      const int kb = ks * 64 + c * 16;
-      const int off = kb < krow ? row * krow + kb : 0x7FFFFFF0;
+      const int row = j * 8 + (lane >> 3);
+      const int kb = ps * 128 + chunk_at(row, lane & 7) * 16, have = is_a ? rows_a : rows_w;
+      const int off = kb < krow ? (row < have ? row : have - 1) * krow + kb : 0x7FFFFFF0;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(is_a ? rA : rW, (lds_ptr_t*)(st + (is_a ? 0 : T::CodesA) + j * 1024), 16,
                                                off, 0, 0, 0);
     } else {
-      const int q = (wave * T::LoadsS + (idx - T::LoadsA - T::LoadsW)) % T::Pieces;  // some twice if uneven
-      const bool is_a = q * 256 < T::ScaleA;
-      const int rel = is_a ? q : q - T::ScaleA / 256;
-      const int off = (rel >> 1) * srow + ks * 512 + (rel & 1) * 256 + lane * 4;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(is_a ? rSA : rSW, (lds_ptr_t*)(st + T::CodesA + T::CodesW + q * 256), 4,
+      const int q = wave % T::Tiles;  // some twice if there are fewer
+      const bool is_a = q < T::TilesA;
+      const int off = 2 * ps + (lane >> 5) < a.groups ? (is_a ? q : q - T::TilesA) * srow + ps * 1024 + lane * 16 : 0x7FFFFFF0;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(is_a ? rSA : rSW, (lds_ptr_t*)(st + T::CodesA + T::CodesW + q * 1024), 16,
                                                off, 0, 0, 0);
     }
   };
-  // half kk: lane half h takes block (chunk) 2 kk + h of the step; fragment f of A, then W
+  // quarter kk: lane half h takes block (chunk) 2 kk + h of the pair; fragment f of A, then W
   auto read_code = [&](int stage, int kk, int f, u32x4_t (&ca)[FM], u32x4_t (&cw)[FN]) __attribute__((always_inline)) {
     const uint8_t* st = smem + stage * T::Stage;
     const int c = 2 * kk + h;
     if (f < FM) {
       const int r = (wm * FM + f) * 32 + lr;
-      ca[f] = *(const u32x4_t*)(st + r * 64 + chunk_at(r, c) * 16);
+      ca[f] = *(const u32x4_t*)(st + r * 128 + chunk_at(r, c) * 16);
     } else {
       const int r = (wn * FN + f - FM) * 32 + lr;
-      cw[f - FM] = *(const u32x4_t*)(st + T::CodesA + r * 64 + chunk_at(r, c) * 16);
+      cw[f - FM] = *(const u32x4_t*)(st + T::CodesA + r * 128 + chunk_at(r, c) * 16);
     }
   };
-  // the four scale bytes of the rows of a side's fragments: 32-row groups lie next to each
-  // other, so a lane's are one run
-  auto read_scales = [&](int stage, bool is_a, uint32_t (&sc)[FM + FN]) __attribute__((always_inline)) {
+  // the four scale bytes, of one step, of the rows of a side's fragments: 32-row groups lie
+  // next to each other, so a lane's are one run
+  auto read_scales = [&](int stage, int step, bool is_a, uint32_t (&sc)[FM + FN]) __attribute__((always_inline)) {
     const int g = is_a ? wm * FM : wn * FN, n = is_a ? FM : FN, at = is_a ? 0 : FM;
-    const uint8_t* p = smem + stage * T::Stage + T::CodesA + T::CodesW + (is_a ? 0 : T::ScaleA) + (g >> 2) * 512 +
-                       lr * 16 + (g & 3) * 4;
+    const uint8_t* p = smem + stage * T::Stage + T::CodesA + T::CodesW + ((is_a ? 0 : T::TilesA) + (g >> 2)) * 1024 +
+                       step * 512 + lr * 16 + (g & 3) * 4;
     if (n == 4) {
       const u32x4_t v = *(const u32x4_t*)p;
 #pragma unroll
@@ -166,7 +169,7 @@ __device__ __forceinline__ void run_tile(const MxGemmArgs& a, int64_t m0, int64_
     }
   };
 
-  constexpr int kEarly = T::Loads / 2;  // loads of a step in its first part
+  constexpr int kEarly = T::Loads / 2;  // loads of a pair in the last quarter before it
   f32x16_t acc[FN][FM];
 #pragma unroll
   for (int j = 0; j < FN; ++j)
@@ -186,54 +189,54 @@ __device__ __forceinline__ void run_tile(const MxGemmArgs& a, int64_t m0, int64_
   uint32_t sc[FM + FN];
 #pragma unroll
   for (int f = 0; f < FM + FN; ++f) read_code(0, 0, f, ca[0], cw[0]);
-  read_scales(0, true, sc);
-  read_scales(0, false, sc);
+  read_scales(0, 0, true, sc);
+  read_scales(0, 0, false, sc);
 
   constexpr int P = FM * FN, F = FM + FN;
-  auto kstep = [&](int ks, int stage) __attribute__((always_inline)) {
-    const int next = stage + 1 == kStages ? 0 : stage + 1, last = stage == 0 ? kStages - 1 : stage - 1;
-    uint32_t hs[F];  // bytes 0 and 2: the lane half's blocks of the two halves
+  uint32_t hs[F];  // bytes 0 and 2: the lane half's blocks of the step's halves
+  // quarter kk of a pair: its products, beside which the next quarter's fragments are read, in
+  // the odd ones the next step's scales, and loads [l0, l1) of pair `to` are issued
+  auto quarter = [&](auto which, int at, int kk_at, int to, int to_stage, int l0, int l1) __attribute__((always_inline)) {
+    constexpr int kk = decltype(which)::value;
+    const int reads = F + (kk & 1 ? 2 : 0);
+    if constexpr ((kk & 1) == 0) {
 #pragma unroll
-    for (int f = 0; f < F; ++f) hs[f] = sc[f] >> (8 * h);
+      for (int f = 0; f < F; ++f) hs[f] = sc[f] >> (8 * h);
+    }
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int j = p / FM, i = p % FM;
-      acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fp4_operand(cw[0][j]), fp4_operand(ca[0][i]),
-                                                                  acc[j][i], 4, 4, 0, (int)hs[FM + j], 0, (int)hs[i]);
+      if constexpr (kk & 1)
+        acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fp4_operand(cw[1][j]), fp4_operand(ca[1][i]),
+                                                                    acc[j][i], 4, 4, 2, (int)hs[FM + j], 2, (int)hs[i]);
+      else
+        acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fp4_operand(cw[0][j]), fp4_operand(ca[0][i]),
+                                                                    acc[j][i], 4, 4, 0, (int)hs[FM + j], 0, (int)hs[i]);
       __builtin_amdgcn_sched_barrier(0);  // its wait for operands comes before the reads below
 #pragma unroll
-      for (int f = 0; f < F; ++f)
-        if (f * (P / 2) / F == p) read_code(stage, 1, f, ca[1], cw[1]);
-#pragma unroll
-      for (int idx = kEarly; idx < T::Loads; ++idx)
-        if ((idx - kEarly) * P / (T::Loads - kEarly) == p) issue(ks - 1 + kStages, last, idx);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this stage's reads are done
-    wait_loads<(kStages - 2) * T::Loads>();
-    barrier();
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int j = p / FM, i = p % FM;
-      acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fp4_operand(cw[1][j]), fp4_operand(ca[1][i]),
-                                                                  acc[j][i], 4, 4, 2, (int)hs[FM + j], 2, (int)hs[i]);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int f = 0; f < F + 2; ++f) {
-        if (f * (P * 3 / 4) / (F + 2) != p) continue;
-        if (f < F) read_code(next, 0, f, ca[0], cw[0]);
-        else read_scales(next, f == F, sc);
+      for (int f = 0; f < reads; ++f) {
+        if (f * (P * 3 / 4) / reads != p) continue;
+        if (f < F) read_code(at, kk_at, f, ca[(kk & 1) ^ 1], cw[(kk & 1) ^ 1]);
+        else read_scales(at, kk_at >> 1, f == F, sc);
       }
 #pragma unroll
-      for (int idx = 0; idx < kEarly; ++idx)
-        if (idx * P / kEarly == p) issue(ks + kStages, stage, idx);
+      for (int idx = l0; idx < l1; ++idx)
+        if ((idx - l0) * P / (l1 - l0) == p) issue(to, to_stage, idx);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  int stage = 0, ks = 0;
-  for (; ks < a.groups; ++ks) {
-    kstep(ks, stage);
-    stage = stage + 1 == kStages ? 0 : stage + 1;
+  const int pairs = (a.groups + 1) / 2;
+  int stage = 0;
+  for (int ps = 0; ps < pairs; ++ps) {
+    const int next = stage + 1 == kStages ? 0 : stage + 1, last = stage == 0 ? kStages - 1 : stage - 1;
+    quarter(std::integral_constant<int, 0>(), stage, 1, ps - 1 + kStages, last, kEarly, T::Loads);
+    quarter(std::integral_constant<int, 1>(), stage, 2, 0, 0, 0, 0);
+    quarter(std::integral_constant<int, 2>(), stage, 3, 0, 0, 0, 0);
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this stage's reads are done
+    wait_loads<(kStages - 2) * T::Loads>();
+    barrier();
+    quarter(std::integral_constant<int, 3>(), next, 0, ps + kStages, stage, 0, kEarly);
+    stage = next;
   }
 
   // ---- epilogue: 32 rows at a time through the wave's part of LDS, so that a store writes
@@ -313,7 +316,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void mx_gemm_kernel(MxGemmArgs a) {
 }
 
 // Parts alone, where there is no whole tile: with registers for themselves they need no moves
-// between the two register files, 24.1 -> 22.8 us for 768 x 5376 x 7168, 33.7 -> 30.5 for 1021.
+// between the two register files, 23.1 -> 20.5 us for 512 x 5376 x 7168, 33.8 -> 29.9 for 1021.
 template <int FM, int FN>
 __global__ __launch_bounds__(64 * kWaves, 2) void mx_gemm_parts_kernel(MxGemmArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
@@ -415,13 +418,13 @@ __global__ __launch_bounds__(64 * W, 2) void mx_gemm_thin_kernel(MxGemmArgs a) {
   }
 }
 
-constexpr int kLds = Shape<4, 4>::Lds;
-static_assert(Shape<2, 4>::Lds <= kLds && Shape<2, 2>::Lds <= kLds, "LDS");
+constexpr int kLds = Shape<2, 4>::Lds;
+static_assert(Shape<4, 4>::Lds <= kLds && Shape<2, 2>::Lds <= kLds && kLds <= 160 * 1024, "LDS");
 
 // Whole rounds of 256 x 256 tiles, which need the fewest operand bytes a product; in a last
 // round (or the only one) that fills at most half of the CUs, 128 x 256 halves, and 128 x 128
-// quarters where even those fill at most half. Measured at K 7168: a round of whole tiles
-// takes 50 us, of halves 28, of quarters 21.
+// quarters where even those fill at most half. Measured at N 5376, K 7168: 168 whole tiles
+// take 48 us, 252 halves 35, 252 quarters 24.
 hipError_t launch_tiles(MxGemmArgs a, hipStream_t stream) {
   a.tiles_m = (int)((a.m + kEdge - 1) / kEdge);
   a.tiles_n = (int)((a.n + kEdge - 1) / kEdge);
