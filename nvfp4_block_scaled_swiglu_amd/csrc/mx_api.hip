@@ -177,13 +177,13 @@ int check_attention(const mxfp4_cache* cache, const mxfp4_batch* batch, int64_t 
     return api_fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "more than 65536 heads, or 2^31 rows x heads of a group");
   *plan = nvfp4::mx_attention_plan(b->tokens, b->batch, heads, c->kv_heads, c->head_dim, max_kv, window, sinks);
   if ((b->tokens * (heads / c->kv_heads) / 16 + b->batch) * c->kv_heads > kMostGroups ||
-      b->tokens * heads > kMostGroups)
+      b->tokens * heads > kMostGroups || (plan->mixed > 0 && b->batch * c->kv_heads * 16 > kMostGroups))
     return api_fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "too many rows and heads for one call");
   return NVFP4_OK;
 }
 
-int64_t workspace_bytes(const nvfp4::MxBatch& b, int64_t heads, int64_t head_dim, const nvfp4::MxAttnPlan& plan) {
-  return plan.splits == 1 ? 0 : plan.splits * b.tokens * heads * (head_dim + 2) * 4;
+int64_t workspace_bytes(const nvfp4::MxBatch& b, const nvfp4::MxCache& c, int64_t heads, const nvfp4::MxAttnPlan& plan) {
+  return nvfp4::mx_part_bytes(plan, b.tokens, b.batch, heads, c.kv_heads, c.head_dim);
 }
 
 }  // namespace
@@ -261,7 +261,7 @@ int64_t mxfp4_attention_workspace_bytes(const mxfp4_cache* cache, const mxfp4_ba
   nvfp4::MxBatch b;
   nvfp4::MxAttnPlan plan;
   if (check_attention(cache, batch, heads, max_kv, window, sinks, &c, &b, &plan) != NVFP4_OK) return -1;
-  return workspace_bytes(b, heads, c.head_dim, plan);
+  return workspace_bytes(b, c, heads, plan);
 }
 
 int mxfp4_attention(const mxfp4_cache* cache, const mxfp4_batch* batch, const void* q_dev, int64_t q_token_stride,
@@ -281,7 +281,7 @@ int mxfp4_attention(const mxfp4_cache* cache, const mxfp4_batch* batch, const vo
     if (rc == NVFP4_OK) rc = check_packed_rows(out_dev, out_token_stride, out_head_stride, "out");
     if (rc == NVFP4_OK) rc = check_written_rows(out_token_stride, out_head_stride, heads, b.tokens, c.head_dim, "out");
     if (rc != NVFP4_OK) return rc;
-    const int64_t need = workspace_bytes(b, heads, c.head_dim, plan);
+    const int64_t need = workspace_bytes(b, c, heads, plan);
     if (need > 0 && !workspace_dev) return api_fail(NVFP4_ERR_WORKSPACE, "null workspace; %lld bytes needed", (long long)need);
     if (workspace_size < need)
       return api_fail(NVFP4_ERR_WORKSPACE, "workspace of %lld bytes; %lld needed", (long long)workspace_size, (long long)need);

@@ -98,9 +98,10 @@ __global__ __launch_bounds__(64 * kWaves, groups_per_cu(D, RT)) void mx_attentio
   const int split = blockIdx.y;
   const int g = a.group;
   // the longest contexts are not known here; the last tiles come first, as in the prompt form
-  const MxRows rows = mx_rows(a, (gridDim.x - 1 - blockIdx.x) / a.c.kv_heads, kRows);
+  const int tile = (gridDim.x - 1 - blockIdx.x) / a.c.kv_heads;
+  const MxRows rows = a.by_seq ? mx_rows_of(a, tile) : mx_rows(a, tile, kRows);
   const int p0 = rows.first;
-  if (p0 >= rows.count) return;  // the whole workgroup
+  if (p0 >= rows.count || (a.by_seq && rows.count > kRows)) return;  // the whole workgroup
   const int p1 = p0 + kRows < rows.count ? p0 + kRows : rows.count;
 
   // ---- the rows ----
@@ -395,7 +396,8 @@ __global__ __launch_bounds__(64 * kWaves, groups_per_cu(D, RT)) void mx_attentio
     const int head = kvh * g + p % g;
     const int e0 = (4 * u + wave) * NJ;
     if (a.splits > 1) {
-      const int64_t at = ((int64_t)split * a.b.tokens + token) * a.heads + head;
+      const int64_t at = a.by_seq ? (((int64_t)split * a.b.batch + rows.seq) * a.c.kv_heads + kvh) * 16 + n
+                                  : ((int64_t)split * a.b.tokens + token) * a.heads + head;
       if (u == 0 && wave == 0) a.part_ml[at] = make_float2(top, sum);
       if (sum != 0.0f) {
 #pragma unroll
@@ -427,10 +429,20 @@ __global__ __launch_bounds__(256) void mx_attention_join_kernel(MxAttnArgs a) {
   __shared__ float red[4];
   __shared__ f32x4_t part[256];
   const int tid = threadIdx.x;
-  const int64_t pair = blockIdx.x, pairs = a.b.tokens * a.heads;
-  const int64_t token = pair / a.heads;
-  const int head = (int)(pair - token * a.heads);
-  if (token < mx_row_start(a.b, 0) || token >= mx_row_start(a.b, a.b.batch)) return;  // of no sequence: stays as it was
+  const int64_t pair = blockIdx.x, pairs = gridDim.x;
+  int64_t token;
+  int head;
+  if (a.by_seq) {
+    const int place = blockIdx.x / 16, n = blockIdx.x % 16, seq = place / a.c.kv_heads;
+    const MxRows rows = mx_rows_of(a, seq);
+    if (n >= rows.count || rows.count > 16) return;  // no such row, or not of this form
+    token = rows.r0 + n / a.group;
+    head = (place - seq * a.c.kv_heads) * a.group + n % a.group;
+  } else {
+    token = pair / a.heads;
+    head = (int)(pair - token * a.heads);
+    if (token < mx_row_start(a.b, 0) || token >= mx_row_start(a.b, a.b.batch)) return;  // of no sequence: stays as it was
+  }
   float2 v = make_float2(-INFINITY, 0.0f);
   if (tid < a.splits) v = a.part_ml[tid * pairs + pair];
   if (v.y == 0.0f) v.x = -INFINITY;  // saw nothing; its o was not written
@@ -472,21 +484,44 @@ __global__ __launch_bounds__(256) void mx_attention_join_kernel(MxAttnArgs a) {
 
 template <int D, int RT>
 hipError_t launch_few(const MxAttnArgs& a, hipStream_t stream) {
-  const int64_t tiles = a.b.tokens * a.group / (16 * RT) + a.b.batch;
+  const int64_t tiles = a.by_seq ? a.b.batch : a.b.tokens * a.group / (16 * RT) + a.b.batch;
   mx_attention_few_kernel<D, RT>
       <<<dim3((unsigned)(tiles * a.c.kv_heads), a.splits), 64 * kWaves, FewLds<D, RT>::Bytes, stream>>>(a);
   return hipGetLastError();
 }
 
 template <int D>
-hipError_t launch_dim(const MxAttnArgs& a, const MxAttnPlan& plan, hipStream_t stream) {
-  hipError_t e;
-  if (!plan.few) e = launch_mx_attention_prompt(a, stream);
-  else if (plan.row_tiles == 1) e = launch_few<D, 1>(a, stream);
-  else e = launch_few<D, D == 64 ? 2 : 1>(a, stream);  // two: only of 64
-  if (e != hipSuccess || a.splits == 1) return e;
-  mx_attention_join_kernel<D><<<(unsigned)(a.b.tokens * a.heads), 256, 0, stream>>>(a);
+hipError_t join(const MxAttnArgs& a, hipStream_t stream) {
+  if (a.splits == 1) return hipSuccess;
+  const int64_t pairs = a.by_seq ? (int64_t)a.b.batch * a.c.kv_heads * 16 : a.b.tokens * a.heads;
+  mx_attention_join_kernel<D><<<(unsigned)pairs, 256, 0, stream>>>(a);
   return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_dim(MxAttnArgs a, const MxAttnPlan& plan, hipStream_t stream) {
+  hipError_t e;
+  if (plan.few) {
+    if (plan.row_tiles == 1) e = launch_few<D, 1>(a, stream);
+    else e = launch_few<D, D == 64 ? 2 : 1>(a, stream);  // two: only of 64
+    return e == hipSuccess ? join<D>(a, stream) : e;
+  }
+  MxAttnArgs few = a;
+  if (plan.mixed > 0) {
+    a.skip = 16;
+    few.by_seq = true;
+    few.splits = plan.mixed;
+    few.part_o = (float*)((uint8_t*)a.part_o + mx_prompt_part_bytes(plan, a.b.tokens, a.heads, D));
+    few.part_ml = (float2*)(few.part_o + (int64_t)plan.mixed * a.b.batch * a.c.kv_heads * 16 * D);
+    e = launch_few<D, 1>(few, stream);
+    if (e != hipSuccess) return e;
+  }
+  e = launch_mx_attention_prompt(a, stream);
+  // Of the few-rows form's sequences the first join writes what nobody left for it; where
+  // there is one (few groups, long caches) those are in pieces too, and the second is right.
+  if (e == hipSuccess) e = join<D>(a, stream);
+  if (e == hipSuccess && plan.mixed > 0) e = join<D>(few, stream);
+  return e;
 }
 
 template <int D, int RT>

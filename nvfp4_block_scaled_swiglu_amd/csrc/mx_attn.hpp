@@ -15,8 +15,10 @@ struct MxAttnArgs {
   float scale_log2;                              // scale * log2 e
   int causal, window, sinks;                     // window 0: none
   int splits;
-  float* part_o;    // [splits, tokens, heads, head_dim]
-  float2* part_ml;  // [splits, tokens, heads] maximum (log2) and sum
+  float* part_o;    // [splits, tokens, heads, head_dim]; by_seq: [splits, batch, kv_heads, 16, head_dim]
+  float2* part_ml;  // [splits, tokens, heads] maximum (log2) and sum; by_seq likewise
+  int skip;         // prompt form: sequences of up to so many packed rows are not its own
+  bool by_seq;      // few-rows form: a workgroup a sequence and kv head, of up to 16 packed rows
 };
 
 constexpr int kMxMostSplits = 256;
@@ -26,6 +28,8 @@ struct MxAttnPlan {
   bool few;       // the form for few rows
   int row_tiles;  // its 16-row tiles of a workgroup
   int splits;     // pieces of the token axis, joined by a second launch
+  int mixed;      // prompt form: its sequences of up to 16 packed rows go to the few-rows form in
+                  // so many pieces; 0: they do not
 };
 
 // Rows: the packed rows (rows x heads of a group) of an average sequence. Up to 16 of them
@@ -46,9 +50,15 @@ struct MxAttnPlan {
 // good. Measured, 32 heads of 128 over 8: 256 rows over 8192 take 177 us whole, 71 with 6
 // splits, 62 with 8, 71 with 16; over 2048: 51, with 3 splits 42, with 4 46; 1024 rows over
 // 1024: 33 whole, 72 with 2.
+//
+// Mixed: a prompt among single tokens makes the average one of prompts, whose form walks a
+// single token's cache with one wave a kv head. Where caches are long a second launch takes
+// the sequences of up to 16 packed rows: 2048 rows over 2048 and 31 single tokens over 8192,
+// 32 heads of 128 over 8, 293 -> 133 us, over 32768 1054 -> 297. Batches without such sequences
+// pay its start; up to 4096 tokens it saves nothing.
 inline MxAttnPlan mx_attention_plan(int64_t tokens, int64_t batch, int64_t heads, int64_t kv_heads, int64_t head_dim,
                                     int64_t max_kv, int64_t window, int64_t sinks) {
-  MxAttnPlan p{true, 1, 1};
+  MxAttnPlan p{true, 1, 1, 0};
   if (tokens <= 0 || batch <= 0) return p;
   const int64_t group = heads / kv_heads;
   const int64_t rows = (tokens + batch - 1) / batch * group;
@@ -76,7 +86,24 @@ inline MxAttnPlan mx_attention_plan(int64_t tokens, int64_t batch, int64_t heads
   if (s > most_splits) s = most_splits;
   if (s > kMxMostSplits) s = kMxMostSplits;
   p.splits = s < 1 ? 1 : (int)s;
+  if (!p.few && batch > 1 && seen > 4096) {
+    s = 2048 / (batch * kv_heads);
+    if (s > seen / (2 * 32 * 4)) s = seen / (2 * 32 * 4);
+    if (s > kMxMostSplits) s = kMxMostSplits;
+    p.mixed = s < 1 ? 1 : (int)s;  // more than 1 wherever p.splits is: batch * kv_heads is below 768 / 2 there
+  }
   return p;
+}
+
+// workspace of the rows' pieces, and of those of the few-rows form's sequences behind it
+inline int64_t mx_prompt_part_bytes(const MxAttnPlan& p, int64_t tokens, int64_t heads, int64_t head_dim) {
+  return p.splits == 1 ? 0 : (p.splits * tokens * heads * (head_dim + 2) * 4 + 15) / 16 * 16;
+}
+
+inline int64_t mx_part_bytes(const MxAttnPlan& p, int64_t tokens, int64_t batch, int64_t heads, int64_t kv_heads,
+                             int64_t head_dim) {
+  return mx_prompt_part_bytes(p, tokens, heads, head_dim) +
+         (p.mixed > 1 ? p.mixed * batch * kv_heads * 16 * (head_dim + 2) * 4 : 0);
 }
 
 hipError_t mx_attention_prompt_setup();
@@ -175,6 +202,19 @@ __device__ __forceinline__ MxRows mx_rows(const MxAttnArgs& a, int64_t tile, int
   const int64_t first = (tile - (r.r0 * a.group / rows + lo)) * rows;
   r.first = first < 0 || first > r.count ? r.count : (int)first;
   r.kv_len = mx_seq_len(a.b, lo);
+  r.back = r.kv_len - (int)(r1 - r.r0);
+  return r;
+}
+
+// all packed rows of a sequence
+__device__ __forceinline__ MxRows mx_rows_of(const MxAttnArgs& a, int seq) {
+  MxRows r;
+  const int64_t r1 = mx_row_start(a.b, seq + 1);
+  r.seq = seq;
+  r.r0 = mx_row_start(a.b, seq);
+  r.count = r1 > r.r0 ? (int)((r1 - r.r0) * a.group) : 0;
+  r.first = 0;
+  r.kv_len = mx_seq_len(a.b, seq);
   r.back = r.kv_len - (int)(r1 - r.r0);
   return r;
 }

@@ -84,7 +84,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D)) void mx_attention_p
   const int g = a.group;
   // within a causal sequence the last tiles see the most tokens: they are started first
   const MxRows rows = mx_rows(a, (gridDim.x - 1 - blockIdx.x) / a.c.kv_heads, kRows);
-  if (rows.first >= rows.count) return;  // the whole workgroup
+  if (rows.first >= rows.count || rows.count <= a.skip) return;  // the whole workgroup
   const int wg_end = rows.first + kRows < rows.count ? rows.first + kRows : rows.count;
   const MxSight all = mx_sight(a, rows, rows.first, wg_end);
   const MxSpan span = mx_span(all, kTile);

@@ -374,3 +374,36 @@ def test_pages_of_two_sequences(gpu, q):
         c.check(nv.mxfp4_attention(c.q, c.cache, table, c.seq, c.cu, max_kv=kv))
     assert nv.mxfp4_attention(own, c.cache, table, c.seq, c.cu, out=own) is own
     c.check(own)
+
+
+@pytest.mark.parametrize("call", [{}, dict(window=5000, sinks=3), dict(causal=False)])
+@pytest.mark.parametrize("kw,lens", [(dict(group=2), [(150, 190), (1, 900), (0, 50), (8, 33), (1, 0), (9, 400)]),
+                                     (dict(group=3, kv_heads=3, dim=64, page=32), [(1, 5000), (100, 100), (5, 2), (2, 1)]),
+                                     (dict(group=16, kv_heads=1, dim=256), [(1, 700), (9, 9), (2, 65)]),
+                                     (dict(group=17, kv_heads=1), [(1, 300), (8, 90)])])
+def test_prompts_among_single_tokens(gpu, kw, lens, call):
+    """Long caches: the sequences of up to 16 rows x heads are the few-rows form's, the others the
+    prompt form's, with and without pieces; and many such sequences, none of them in pieces."""
+    import torch
+    import nvfp4_block_scaled_swiglu_amd as nv
+    c = Case(gpu, lens, **kw).fill(gpu)
+    args = (c.cache, c.table, c.seq, c.cu)
+    assert nv.mxfp4_attention_workspace_bytes(*args, c.tokens, c.heads, 1 << 13) > 0
+    out = nv.mxfp4_attention(c.q, *args, max_kv=1 << 13, **call)
+    c.check(out, **call)
+    assert torch.equal(out, nv.mxfp4_attention(c.q, *args, max_kv=1 << 13, **call))
+    c.check(nv.mxfp4_attention(c.q, *args, max_kv=1 << 17, **call), **call)
+    own = torch.cat([c.q, torch.full_like(c.q[:2], 7.0)])  # its own output, with rows of no sequence
+    nv.mxfp4_attention(own, *args, max_kv=1 << 17, out=own, **call)
+    c.check(own[:c.tokens], **call)
+    assert (own[c.tokens:] == 7.0).all()
+
+
+@pytest.mark.parametrize("kv_heads,singles,prompt", [(2, 520, 3000), (8, 139, 600)])
+def test_many_single_tokens_and_a_prompt(gpu, kv_heads, singles, prompt):
+    """520: so many that the average makes it one launch of the few-rows form, the prompt with it.
+    139 of 8 heads: the prompt form, and as many workgroups of the other as are wanted already."""
+    import nvfp4_block_scaled_swiglu_amd as nv
+    lens = [(1, 3 + i % 40) for i in range(singles)] + [(prompt, prompt)] + [(1, 20)] * 9
+    c = Case(gpu, lens, group=4, dim=64, kv_heads=kv_heads).fill(gpu)
+    c.check(nv.mxfp4_attention(c.q, c.cache, c.table, c.seq, c.cu, max_kv=1 << 13))
