@@ -44,12 +44,12 @@ struct MxAttnPlan {
 // rounds of them: 48 tokens over up to 8200 take 80 us with 5 splits, 94 with 2, 86 with 10),
 // but at least two 32-token tiles a wave, so that a split is more than its own start.
 // Prompts: as many as are resident at once, by registers 3, 2 or 1 a CU. But a split writes
-// and reads every row once more in fp32, about head_dim tokens heads splits * 2.6 ps, which it
+// and reads every row once more in fp32, about head_dim tokens heads splits * 1.3 ps, which it
 // has to save of the head_dim / 6 ns that a workgroup takes for a token: the sum is least at
-// sqrt(64 seen / (tokens heads)) splits, and below three of them not splitting is as good.
-// Measured, 32 heads of 128 over 8: 256 rows over 8192 take 177 us whole, 71 with 6 splits, 62
-// with 8, 71 with 16; over 2048: 51, with 3 splits 42, with 4 46; 1024 rows over 1024: 33
-// whole, 72 with 2. 28 over 4, 904 rows over up to 3656: 122 whole, 101 with 3, 98 with 5.
+// sqrt(128 seen / (tokens heads)) splits, and below three of them not splitting is as good.
+// Measured, 32 heads of 128 over 8: 256 rows over 8192 take 180 us whole, 62 with 6 splits, 57
+// with 8, 66 with 12; over 1024: 31 whole, 24 with 3; 1024 rows over 1024: 33 whole, 45 with
+// 2. 28 heads over 4, 904 rows over up to 3656: 122 whole, 84 with 3, 82 with 4.
 //
 // Mixed: a prompt among single tokens makes the average one of prompts, whose form walks a
 // single token's cache with one wave a kv head. Where caches are long a second launch takes
@@ -80,7 +80,7 @@ inline MxAttnPlan mx_attention_plan(int64_t tokens, int64_t batch, int64_t heads
   } else {
     s = (head_dim == 64 ? 768 : head_dim == 128 ? 512 : 256) / groups;
     most_splits = 2;
-    while ((most_splits + 1) * (most_splits + 1) * tokens * heads <= 64 * seen && most_splits < kMxMostSplits) ++most_splits;
+    while ((most_splits + 1) * (most_splits + 1) * tokens * heads <= 128 * seen && most_splits < kMxMostSplits) ++most_splits;
     if (most_splits < 3) most_splits = 1;
   }
   if (s > most_splits) s = most_splits;
