@@ -14,7 +14,7 @@
 // with direct-to-LDS loads that need no register while they fly and no barrier (six
 // instructions for 32 tokens of 128 elements, every one of whole runs): 16 waves x 2 slots
 // x 4.25 KiB in flight per CU. 48 single tokens over up to 8200, 56 heads of 128 over 8: 78
-// us and 7 of joining, 4.2 TB/s of the cache; the loads alone take 63, the rest alone 69.
+// us and 5 of joining, 4.2 TB/s of the cache; the loads alone take 63, the rest alone 69.
 //
 // One pass with the running maximum and sum of the softmax, in the transposed form with
 // v_mfma_f32_16x16x32_bf16, lane (n, u) = (lane & 15, lane >> 4):
