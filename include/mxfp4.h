@@ -161,7 +161,8 @@ int64_t mxfp4_attention_workspace_bytes(const mxfp4_cache* cache, const mxfp4_ba
  *                  were. The rows' own keys and values are in the cache already
  *                  (mxfp4_cache_append with the same batch, before).
  * heads          : a multiple of kv_heads, at most 65536; tokens * heads / kv_heads < 2^31.
- * scale          : finite, > 0.
+ * scale          : > 0, at most 2^127. Scores q . k are fp32 sums and have to lie in its range;
+ *                  scale times them need not.
  * window, sinks  : >= 0; a window needs causal, sinks need a window.
  * max_kv         : the longest cache of the batch as far as the caller knows (> 0). It only
  *                  decides how the work is split, not the result's meaning.

@@ -273,7 +273,7 @@ int mxfp4_attention(const mxfp4_cache* cache, const mxfp4_batch* batch, const vo
   nvfp4::MxAttnPlan plan;
   int rc = check_attention(cache, batch, heads, max_kv, window, sinks, &c, &b, &plan);
   if (rc != NVFP4_OK) return rc;
-  if (!std::isfinite(scale) || scale <= 0.0f) return api_fail(NVFP4_ERR_INVALID_ARG, "scale must be finite and positive");
+  if (!(scale > 0.0f && scale <= 0x1p127f)) return api_fail(NVFP4_ERR_INVALID_ARG, "scale must be positive, at most 2^127");
   if (window > 0 && !causal) return api_fail(NVFP4_ERR_INVALID_ARG, "a window needs causal attention");
   const bool any = b.tokens > 0 && b.batch > 0;
   if (any) {
@@ -303,6 +303,7 @@ int mxfp4_attention(const mxfp4_cache* cache, const mxfp4_batch* batch, const vo
   a.heads = (int)heads;
   a.group = (int)(heads / c.kv_heads);
   a.scale_log2 = scale * 1.44269504f;
+  a.raise = nvfp4::kMxRaise / a.scale_log2;
   // lengths stay below 2^30: a window or first tokens beyond that hide nothing more
   a.causal = causal != 0;
   a.window = (int)(window < (1 << 30) ? window : 1 << 30);

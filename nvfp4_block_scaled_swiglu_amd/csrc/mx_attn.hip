@@ -35,9 +35,9 @@
 // for the product (2^-8 of each weight at most, the size of o's own rounding); its sum is of
 // the same rounded weights, so that they still add up to one.
 //
-// The maximum is raised only when a score exceeds it by more than 2^8: until then weights
-// up to 2^8 are as exact as those below 1, and most tiles skip the cross-lane maximum and
-// the rescaling of O.
+// The maximum is raised only when a weight under it would exceed 2^8: until then weights up to
+// 2^8 are as exact as those below 1, and most tiles skip the cross-lane maximum and the
+// rescaling of O.
 #include <type_traits>
 
 #include "mx_attn.hpp"
@@ -192,11 +192,13 @@ __global__ __launch_bounds__(64 * kWaves, groups_per_cu(D, RT)) void mx_attentio
 
   // ---- state ----
   f32x4_t o[RT][NJ];
-  float m[RT], l[RT];  // m: agreed by the four lanes of a row; l: the lane's own tokens
+  float m[RT], l[RT];       // m: the reference score, agreed by the four lanes of a row; l: the lane's own tokens
+  float neg[RT], most[RT];  // of its unit; the score up to which it stays
+  bool far = false;         // some row's reference is
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
-    m[r] = -INFINITY;
-    l[r] = 0.0f;
+    m[r] = most[r] = -INFINITY;
+    l[r] = neg[r] = 0.0f;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) o[r][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   }
@@ -240,22 +242,27 @@ __global__ __launch_bounds__(64 * kWaves, groups_per_cu(D, RT)) void mx_attentio
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
       float top = fmaxf(fmaxf(fmaxf(s[r][0][0], s[r][0][1]), fmaxf(s[r][0][2], s[r][0][3])),
-                        fmaxf(fmaxf(s[r][1][0], s[r][1][1]), fmaxf(s[r][1][2], s[r][1][3]))) * a.scale_log2;
-      if (__any(top > m[r] + kMxRaise)) {
+                        fmaxf(fmaxf(s[r][1][0], s[r][1][1]), fmaxf(s[r][1][2], s[r][1][3])));
+      if (far | __any(!(top <= most[r]))) {
         top = fmaxf(top, __shfl_xor(top, 16, 64));
         top = fmaxf(top, __shfl_xor(top, 32, 64));
         const float next = fmaxf(m[r], top);
-        const float f = m[r] == next ? 1.0f : __builtin_amdgcn_exp2f(m[r] - next);  // m = -inf: o and l are 0
+        const MxUnit unit = mx_unit(a, next);
+        far |= __any(unit.far);
+        const float f = mx_rebase(a, m[r], next);  // m = -inf: o and l are 0
         m[r] = next;
+        neg[r] = unit.neg;
+        most[r] = next == -INFINITY ? -INFINITY : next + a.raise;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) s[r][h] -= unit.base;  // 0 unless far, when every step comes here
         l[r] *= f;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) o[r][j] *= f;
       }
-      const float neg = m[r] == -INFINITY ? 0.0f : -m[r];  // nothing seen yet: every weight is exp2(-inf)
       float p[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        p[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][j >> 2][j & 3], a.scale_log2, neg));
+        p[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][j >> 2][j & 3], a.scale_log2, neg[r]));
       uint32_t w[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -375,7 +382,7 @@ __global__ __launch_bounds__(64 * kWaves, groups_per_cu(D, RT)) void mx_attentio
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
       const float mw = ml[(w * RT + r) * 16 + n];
-      f[w] = mw == top ? 1.0f : __builtin_amdgcn_exp2f(mw - top);
+      f[w] = mx_rebase(a, mw, top);
       sum += f[w] * ml[(kWaves * RT + w * RT + r) * 16 + n];
     }
 #pragma unroll
@@ -455,7 +462,7 @@ __global__ __launch_bounds__(256) void mx_attention_join_few_kernel(MxAttnArgs a
 #pragma unroll
   for (int off = kJoinWave / 2; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
   top = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(top)));
-  const float f = v.y == 0.0f ? 0.0f : v.x == top ? 1.0f : __builtin_amdgcn_exp2f(v.x - top);
+  const float f = v.y == 0.0f ? 0.0f : mx_rebase(a, v.x, top);
   float sum = v.y == 0.0f ? 0.0f : f * v.y;
 #pragma unroll
   for (int off = kJoinWave / 2; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
@@ -516,7 +523,7 @@ __global__ __launch_bounds__(256) void mx_attention_join_kernel(MxAttnArgs a) {
     return max ? fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])) : (red[0] + red[1]) + (red[2] + red[3]);
   };
   const float top = all(v.x, true);
-  const float f = v.y == 0.0f ? 0.0f : v.x == top ? 1.0f : __builtin_amdgcn_exp2f(v.x - top);
+  const float f = v.y == 0.0f ? 0.0f : mx_rebase(a, v.x, top);
   const float sum = all(v.y == 0.0f ? 0.0f : f * v.y, false);
   if (tid < a.splits) weight[tid] = v.y == 0.0f ? -1.0f : f;
   __syncthreads();

@@ -12,11 +12,11 @@ struct MxAttnArgs {
   uint16_t* out;
   int64_t q_token, q_head, out_token, out_head;  // element strides
   int heads, group;                              // group = heads / kv_heads
-  float scale_log2;                              // scale * log2 e
+  float scale_log2, raise;                       // scale * log2 e; kMxRaise / scale_log2
   int causal, window, sinks;                     // window 0: none
   int splits;
   float* part_o;    // [splits, tokens, heads, head_dim]; by_seq: [splits, batch, kv_heads, 16, head_dim]
-  float2* part_ml;  // [splits, tokens, heads] maximum (log2) and sum; by_seq likewise
+  float2* part_ml;  // [splits, tokens, heads] reference score and sum; by_seq likewise
   int skip;         // prompt form: sequences of up to so many packed rows are not its own
   bool by_seq;      // few-rows form: a workgroup a sequence and kv head, of up to 16 packed rows
 };
@@ -112,6 +112,36 @@ hipError_t launch_mx_attention_prompt(const MxAttnArgs& a, hipStream_t stream);
 // ---- device side ----
 
 constexpr float kMxRaise = 8.0f;  // log2 of how far weights may exceed 1 before the maximum is raised
+
+// Weights are powers of two under a reference score t, the largest of the row so far. While
+// |scale_log2 t| is below 2^20 their unit is that of fl(scale_log2 t): one fma gives a weight's
+// exponent with one rounding, and the reference's own, 2^-5 at most, only puts the largest
+// weight that far from 1. Beyond, it would put it anywhere (2^+-128 at 2^31), or scale_log2 t be
+// infinite: there the unit is that of t itself, and t is taken off first, which is exact for
+// scores that count. A reference of -inf has seen nothing.
+constexpr float kMxNear = 0x1p20f;
+
+struct MxUnit {
+  float base, neg;  // a weight's exponent: scale_log2 (x - base) + neg
+  bool far;
+};
+
+__device__ __forceinline__ MxUnit mx_unit(const MxAttnArgs& a, float t) {
+  const float e = t * a.scale_log2;
+  const bool none = t == -INFINITY, far = !none && !(fabsf(e) < kMxNear);
+  return MxUnit{far ? t : 0.0f, far || none ? 0.0f : -e, far};
+}
+
+// What weights and their sums under reference t are multiplied with to be under reference u >= t;
+// 1 if there are none. (A quick way out where no lane is far costs more than it saves: the prompt
+// form of 64 then spills, 99 us for 91.)
+__device__ __forceinline__ float mx_rebase(const MxAttnArgs& a, float t, float u) {
+  const MxUnit from = mx_unit(a, t);
+  const float off = from.far ? 0.0f : __builtin_fmaf(t, a.scale_log2, from.neg);  // of t from its unit
+  if (t == u || t == -INFINITY) return 1.0f;
+  const MxUnit to = mx_unit(a, u);
+  return __builtin_amdgcn_exp2f(__builtin_fmaf(t - to.base, a.scale_log2, to.neg) - off);
+}
 
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8_t;
 typedef __attribute__((ext_vector_type(4))) float f32x4_t;

@@ -64,7 +64,8 @@ struct Lds {
   static constexpr int KRow = D * 2 + 16;
   static constexpr int K = kTile * KRow, V = D * kTile * 2;   // bytes of a tile
   static constexpr int Nan = D / 32 * kTile;                  // V bytes that are NaN, [block][token]
-  static constexpr int VAt = 2 * K, NanAt = VAt + 2 * V, FlagAt = NanAt + 2 * Nan, Bytes = FlagAt + 2 * 4 * kWaves;
+  static constexpr int VAt = 2 * K, NanAt = VAt + 2 * V, FlagAt = NanAt + 2 * Nan;
+  static constexpr int RefAt = FlagAt + 2 * 4 * kWaves, Bytes = RefAt + 64 * kWaves * 4;  // reference scores, by lane
   static_assert(Bytes <= 160 * 1024, "LDS");
 };
 
@@ -215,12 +216,16 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D)) void mx_attention_p
   // ---- state ----
   f32x16_t o[DB];
   f32x16_t s0, s1;  // scores of a tile's halves
-  float m = -INFINITY, l = 0.0f;
+  float neg = 0.0f, l = 0.0f;  // the unit of the reference score, the sum of the lane's tokens
+  // the score itself is needed when it is raised, and waits in LDS (in a register instead of neg,
+  // its unit taken in every half: D = 64 spills, 100 us for 91)
+  float* const ref = (float*)(smem + L::RefAt) + (wave * 64 + h * 32 + n);
+  *ref = -INFINITY;
 #pragma unroll
   for (int d = 0; d < DB; ++d)
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
-  bool fresh = true;  // some row has seen nothing yet
+  bool wary = true;  // some row has seen nothing yet, or its reference is far
 
   bf16x8_t kf[KS], vf[KS];  // fragments of a half: K by step, V by (16 tokens, block)
   auto read_k = [&](int buf, int half, int k) __attribute__((always_inline)) {
@@ -255,7 +260,6 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D)) void mx_attention_p
   float sum;       // of the lane's 16
   // weights 4 j .. 4 j + 3: taken (the exponentials), then summed and packed
   auto take = [&](const f32x16_t& x, int j, float (&p)[4]) __attribute__((always_inline)) {
-    const float neg = m == -INFINITY ? 0.0f : -m;  // nothing seen yet: every weight is exp2(-inf)
 #pragma unroll
     for (int i = 0; i < 4; ++i) p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[4 * j + i], a.scale_log2, neg));
   };
@@ -269,16 +273,18 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D)) void mx_attention_p
   };
   // after the weights of x: raises the maximum and takes them again if that is due
   bf16x8_t pf[2];
-  auto settle = [&](const f32x16_t& x) __attribute__((always_inline)) {
-    if (__any(fresh | !(sum <= kMostSum))) {
+  auto settle = [&](f32x16_t& x) __attribute__((always_inline)) {
+    if (__any(wary | !(sum <= kMostSum))) {
       float top = x[0];
 #pragma unroll
       for (int i = 1; i < 16; ++i) top = fmaxf(top, x[i]);
-      top *= a.scale_log2;
-      const float next = fmaxf(m, fmaxf(top, __shfl_xor(top, 32, 64)));
-      const float f = m == next ? 1.0f : __builtin_amdgcn_exp2f(m - next);  // m = -inf: o and l are 0
-      m = next;
-      fresh = __any((next == -INFINITY) & (high > 0));
+      const float m = *ref, next = fmaxf(m, fmaxf(top, __shfl_xor(top, 32, 64)));
+      const float f = mx_rebase(a, m, next);  // m = -inf: o and l are 0
+      *ref = next;
+      const MxUnit unit = mx_unit(a, next);
+      neg = unit.neg;
+      wary = __any(((next == -INFINITY) & (high > 0)) | unit.far);
+      x -= unit.base;  // 0 unless far, when every half comes here
       l *= f;
 #pragma unroll
       for (int d = 0; d < DB; ++d) o[d] *= f;
@@ -443,7 +449,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D)) void mx_attention_p
   const int head = kvh * g + pn % g;
   if (a.splits > 1) {
     const int64_t at = ((int64_t)split * a.b.tokens + token) * a.heads + head;
-    if (h == 0) a.part_ml[at] = make_float2(m, all_sum);
+    if (h == 0) a.part_ml[at] = make_float2(*ref, all_sum);
     if (all_sum != 0.0f) {
 #pragma unroll
       for (int d = 0; d < DB; ++d)

@@ -385,7 +385,7 @@ def mxfp4_attention(q, cache: Mxfp4Cache, block_table, seq_lens, cu_seqlens, sca
     their sequences; heads a multiple of the cache's kv_heads, which query heads share in order.
 
     causal: a row sees the tokens up to its own position. window > 0: of those only the last
-    `window`, and the first `sinks` tokens. scale: by default head_dim ** -0.5. max_kv: the
+    `window`, and the first `sinks` tokens. scale: up to 2^127, by default head_dim ** -0.5. max_kv: the
     longest cached length as far as known (by default what the block table could hold); it
     decides how the work is split. workspace: a uint8 tensor of at least
     mxfp4_attention_workspace_bytes(...) bytes, allocated by default. Rows that see nothing give
