@@ -13,7 +13,8 @@ As elsewhere in the package every step runs in the library's kernels, a failing 
 (strict) or returns None and counts a fallback, and outputs that the caller does not pass are
 allocated with torch. Calls run on the device of their tensors (which must be one) and on
 ``stream``, by default that device's current stream; with another stream given, outputs and
-workspaces are allocated for it and the inputs are marked as used by it.
+workspaces are allocated for it, and the tensors that the caller passes (inputs, outputs and
+workspaces) are marked as used by it.
 
 A packed batch is described by ``block_table`` (int32 [batch, max_pages]: page numbers),
 ``seq_lens`` (int32 [batch]: cached tokens of each sequence, the call's new ones included) and
@@ -197,7 +198,7 @@ def _current_stream(index: int) -> int:
 class _On:
     """The device and stream of a call: enter it to allocate outputs and to launch."""
 
-    __slots__ = ("device", "handle", "stack")
+    __slots__ = ("device", "handle", "stack", "side")
 
     def __init__(self, stream, *tensors):
         import torch
@@ -206,7 +207,7 @@ class _On:
             if t.get_device() != index:
                 raise ValueError("all tensors of a call must be on one device")
         self.device = tensors[0].device
-        self.stack = None
+        self.stack = self.side = None
         if stream is None and index == torch.cuda.current_device():  # nothing to switch
             self.handle = _current_stream(index)
             return
@@ -218,13 +219,18 @@ class _On:
                 if getattr(stream, "device", self.device) != self.device:
                     raise ValueError("stream is of another device than the tensors")
                 self.stack.enter_context(torch.cuda.stream(stream))
-                for t in tensors:
-                    t.record_stream(stream)
-                current = stream
+                self.side = current = stream
+                self.use(*tensors)
             self.handle = int(current.cuda_stream)
         except BaseException:
             self.stack.close()
             raise
+
+    def use(self, *tensors):
+        """Marks the caller's tensors as used by the call's stream if that is not the current one."""
+        if self.side is not None:
+            for t in tensors:
+                t.record_stream(self.side)
 
     def __enter__(self):
         return self
@@ -236,12 +242,14 @@ class _On:
 
 # ---- quantization --------------------------------------------------------------------------
 
-def _quantize_out(out, rows: int, k: int, device):
+def _quantize_out(on: _On, out, rows: int, k: int):
+    device = on.device
     if out is None:
         return empty_mxfp4(rows, k, device)
     _packed(out, "out")
     if out.rows != rows or out.k != k or out.qdata.device != device or out.scales.device != device:
         raise ValueError("out must be an Mxfp4Tensor for the same rows and k on the same device")
+    on.use(out.qdata, out.scales)
     return out
 
 
@@ -251,7 +259,7 @@ def mxfp4_quantize(x, out: Optional[Mxfp4Tensor] = None, stream=None,
     _bf16(x, "x", 2)
     rows, k = x.shape
     with _On(stream, x) as on:
-        out = _quantize_out(out, rows, k, x.device)
+        out = _quantize_out(on, out, rows, k)
         if not nv._call("mxfp4_quantize", x.data_ptr(), _row_stride(x), rows, k, out.qdata.data_ptr(),
                         out.scales.data_ptr(), on.handle, strict=strict):
             return None
@@ -265,7 +273,7 @@ def mxfp4_quantize_swiglu(gate, up, out: Optional[Mxfp4Tensor] = None, stream=No
     _bf16(up, "up", 2, gate.shape)
     m, k = gate.shape
     with _On(stream, gate, up) as on:
-        out = _quantize_out(out, m, k, gate.device)
+        out = _quantize_out(on, out, m, k)
         if not nv._call("mxfp4_quantize_swiglu", gate.data_ptr(), _row_stride(gate), up.data_ptr(), _row_stride(up), m, k,
                         out.qdata.data_ptr(), out.scales.data_ptr(), on.handle, strict=strict):
             return None
@@ -281,6 +289,8 @@ def mxfp4_dequantize(t: Mxfp4Tensor, out=None, stream=None, strict: Optional[boo
             out = torch.empty((t.rows, t.k), dtype=torch.bfloat16, device=on.device)
         elif _bf16(out, "out", 2, (t.rows, t.k)).device != on.device:
             raise ValueError("out must be on the device of t")
+        else:
+            on.use(out)
         if not nv._call("mxfp4_dequantize", t.qdata.data_ptr(), t.scales.data_ptr(), t.rows, t.k, out.data_ptr(),
                         _row_stride(out), on.handle, strict=strict):
             return None
@@ -302,6 +312,8 @@ def mxfp4_gemm_bf16out(a: Mxfp4Tensor, w: Mxfp4Tensor, out=None, stream=None, st
             out = torch.empty((m, n), dtype=torch.bfloat16, device=on.device)
         elif _bf16(out, "out", 2, (m, n)).device != on.device:
             raise ValueError("out must be on the device of a and w")
+        else:
+            on.use(out)
         if not nv._call("mxfp4_gemm_bf16out", a.qdata.data_ptr(), a.scales.data_ptr(), w.qdata.data_ptr(),
                         w.scales.data_ptr(), out.data_ptr(), out.stride(0) if m > 1 else n, m, n, a.k, on.handle,
                         strict=strict):
@@ -367,11 +379,14 @@ def mxfp4_cache_read(cache: Mxfp4Cache, block_table, seq_lens, cu_seqlens, token
     b, bt = _batch(block_table, seq_lens, cu_seqlens, tokens)
     shape = (tokens, c.kv_heads, c.head_dim)
     with _On(stream, *ct, *bt) as on:
+        made = None
         if out is None:
-            out = tuple(torch.empty(shape, dtype=torch.bfloat16, device=on.device) for _ in range(2))
-        k, v = out
+            made = tuple(torch.empty(shape, dtype=torch.bfloat16, device=on.device) for _ in range(2))
+        k, v = made or out
         if _bf16(k, "out k", 3, shape).device != on.device or _bf16(v, "out v", 3, shape).device != on.device:
             raise ValueError("out must be on the device of the cache")
+        if made is None:
+            on.use(k, v)
         if not nv._call("mxfp4_cache_read", c, b, k.data_ptr(), *_strides(k), v.data_ptr(), *_strides(v), on.handle,
                         strict=strict):
             return None
@@ -406,12 +421,16 @@ def mxfp4_attention(q, cache: Mxfp4Cache, block_table, seq_lens, cu_seqlens, sca
             out = torch.empty((tokens, heads, dim), dtype=torch.bfloat16, device=on.device)
         elif _bf16(out, "out", 3, q.shape).device != on.device:
             raise ValueError("out must be on the device of q")
+        else:
+            on.use(out)
         if workspace is None:
             size = nv.lib().mxfp4_attention_workspace_bytes(c, b, heads, max_kv, window, sinks)
             if size > 0:
                 workspace = torch.empty((size,), dtype=torch.uint8, device=on.device)
         elif _buffer(workspace, "workspace", 0).device != on.device:
             raise ValueError("workspace must be on the device of q")
+        else:
+            on.use(workspace)
         if not nv._call("mxfp4_attention", c, b, q.data_ptr(), *_strides(q), heads, scale, int(bool(causal)), window, sinks,
                         max_kv, out.data_ptr(), *_strides(out), 0 if workspace is None else workspace.data_ptr(),
                         0 if workspace is None else workspace.numel(), on.handle, strict=strict):
