@@ -160,7 +160,8 @@ int64_t mxfp4_attention_workspace_bytes(const mxfp4_cache* cache, const mxfp4_ba
  *                  multiples of 8); 16-byte aligned. Rows of no sequence are left as they
  *                  were. The rows' own keys and values are in the cache already
  *                  (mxfp4_cache_append with the same batch, before).
- * heads          : a multiple of kv_heads, at most 65536; tokens * heads / kv_heads < 2^31.
+ * heads          : a multiple of kv_heads, at most 65536; tokens * heads / kv_heads < 2^31 and
+ *                  (tokens * heads / kv_heads / 16 + batch) * kv_heads < 2^24.
  * scale          : > 0, at most 2^127. Scores q . k are fp32 sums and have to lie in its range;
  *                  scale times them need not.
  * window, sinks  : >= 0; a window needs causal, sinks need a window.

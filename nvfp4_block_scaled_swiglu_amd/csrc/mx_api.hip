@@ -173,12 +173,12 @@ int check_attention(const mxfp4_cache* cache, const mxfp4_batch* batch, int64_t 
   if (window < 0 || sinks < 0 || (sinks > 0 && window == 0))
     return api_fail(NVFP4_ERR_INVALID_ARG, "window=%lld sinks=%lld (sinks need a window)", (long long)window,
                     (long long)sinks);
-  if (heads > 65536 || b->tokens * (heads / c->kv_heads) >= (int64_t)1 << 31)
-    return api_fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "more than 65536 heads, or 2^31 rows x heads of a group");
-  *plan = nvfp4::mx_attention_plan(b->tokens, b->batch, heads, c->kv_heads, c->head_dim, max_kv, window, sinks);
-  if ((b->tokens * (heads / c->kv_heads) / 16 + b->batch) * c->kv_heads > kMostGroups ||
-      b->tokens * heads > kMostGroups || (plan->mixed > 0 && b->batch * c->kv_heads * 16 > kMostGroups))
+  // The workgroups of a launch: 16 packed rows each at least. (Joins have fewer: pieces are made
+  // only where there are no 2048 workgroups of up to 32 rows, or 768 of 128.)
+  const int64_t packed = heads > 65536 ? -1 : b->tokens * (heads / c->kv_heads);
+  if (packed < 0 || packed >= (int64_t)1 << 31 || (packed / 16 + b->batch) * c->kv_heads > kMostGroups)
     return api_fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "too many rows and heads for one call");
+  *plan = nvfp4::mx_attention_plan(b->tokens, b->batch, heads, c->kv_heads, c->head_dim, max_kv, window, sinks);
   return NVFP4_OK;
 }
 

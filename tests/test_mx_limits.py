@@ -24,3 +24,22 @@ def test_largest_scale(no_gpu):
     assert attention(dict(scale=2.0 ** 127)) == NO_DEVICE
     assert attention(dict(scale=1.5 * 2.0 ** 127)) == 1
     assert attention(dict(scale=2.0 ** -149)) == NO_DEVICE
+
+
+@pytest.mark.parametrize("kw,status", [
+    # what the sizes of a launch allow: (tokens * heads / kv_heads / 16 + batch) * kv_heads below 2^24
+    (dict(b_tokens=262144, b_batch=1, c_heads=8, heads=64), NO_DEVICE),
+    (dict(b_tokens=262144, b_batch=262144, c_heads=8, heads=64), NO_DEVICE),
+    (dict(b_tokens=1 << 24, b_batch=1, c_heads=1, heads=8), NO_DEVICE),
+    (dict(b_tokens=(1 << 24) - 17, b_batch=1, c_heads=1, heads=16), NO_DEVICE),
+    (dict(b_tokens=(1 << 24) - 1, b_batch=1, c_heads=1, heads=16), 2),
+    (dict(b_tokens=1, b_batch=1 << 21, c_heads=8, heads=8), 2),
+    (dict(b_tokens=1 << 24, b_batch=1, c_heads=1, heads=128), 2),  # rows x heads of a group: 2^31
+])
+def test_rows_and_heads_of_an_attention(no_gpu, kw, status):
+    wide = dict(qt=1 << 20, ot=1 << 20)
+    assert attention({**wide, **kw}) == status
+    c, b = structs(kw)
+    size = nv.lib().mxfp4_attention_workspace_bytes(c, b, kw["heads"], 32, 0, 0)
+    assert size == (0 if status == NO_DEVICE else -1)
+
