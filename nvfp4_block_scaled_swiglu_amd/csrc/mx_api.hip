@@ -15,6 +15,7 @@ hipError_t launch_mx_quantize(const uint16_t* x, int64_t ldx, const uint16_t* up
                               uint8_t* qdata, uint8_t* scales, const uint16_t* silu_table, hipStream_t stream);
 hipError_t launch_mx_dequantize(const uint8_t* qdata, const uint8_t* scales, uint16_t* y, int64_t ldy, int64_t m,
                                 int64_t k, hipStream_t stream);
+int64_t mx_cache_groups(int64_t tokens, int64_t head_dim);
 hipError_t launch_mx_cache_append(const MxBatch& b, const MxCache& c, const uint16_t* k, int64_t k_token,
                                   int64_t k_head, const uint16_t* v, int64_t v_token, int64_t v_head,
                                   hipStream_t stream);
@@ -146,7 +147,9 @@ int move_cache(bool append, const mxfp4_cache* cache, const mxfp4_batch* batch, 
   nvfp4::MxBatch b;
   int rc = check_cache(cache, batch, &c, &b);
   const bool any = rc == NVFP4_OK && b.tokens > 0 && b.batch > 0;
-  if (any) rc = check_packed_rows(k, kt, kh, "k");
+  if (any && nvfp4::mx_cache_groups(b.tokens, c.head_dim) > kMostGroups)
+    rc = api_fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "too many rows for one call (%lld)", (long long)b.tokens);
+  if (any && rc == NVFP4_OK) rc = check_packed_rows(k, kt, kh, "k");
   if (any && rc == NVFP4_OK) rc = check_packed_rows(v, vt, vh, "v");
   if (any && rc == NVFP4_OK && !append) rc = check_written_rows(kt, kh, c.kv_heads, b.tokens, c.head_dim, "k");
   if (any && rc == NVFP4_OK && !append) rc = check_written_rows(vt, vh, c.kv_heads, b.tokens, c.head_dim, "v");

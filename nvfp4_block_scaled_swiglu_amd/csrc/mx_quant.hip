@@ -248,11 +248,20 @@ __global__ __launch_bounds__(kThreads) void mx_cache_kernel(CacheArgs a) {
   }
 }
 
+}  // namespace
+
+// workgroups along the tokens
+int64_t mx_cache_groups(int64_t tokens, int64_t head_dim) {
+  const int64_t rows = kThreads / (head_dim / 8);
+  return (tokens + rows - 1) / rows;
+}
+
+namespace {
+
 template <bool WRITE>
 hipError_t launch_cache(CacheArgs a, hipStream_t stream) {
-  const int rows = kThreads / (a.c.head_dim / 8);
   a.head_groups = (a.c.kv_heads + kHeads - 1) / kHeads;
-  const dim3 grid((unsigned)((a.b.tokens + rows - 1) / rows), 2 * a.head_groups);
+  const dim3 grid((unsigned)mx_cache_groups(a.b.tokens, a.c.head_dim), 2 * a.head_groups);
   switch (a.c.head_dim) {
     case 64: mx_cache_kernel<64, WRITE><<<grid, kThreads, 0, stream>>>(a); break;
     case 128: mx_cache_kernel<128, WRITE><<<grid, kThreads, 0, stream>>>(a); break;

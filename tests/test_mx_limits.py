@@ -43,3 +43,13 @@ def test_rows_and_heads_of_an_attention(no_gpu, kw, status):
     size = nv.lib().mxfp4_attention_workspace_bytes(c, b, kw["heads"], 32, 0, 0)
     assert size == (0 if status == NO_DEVICE else -1)
 
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_rows_of_a_cache_call(no_gpu, dim):
+    """A launch takes 2^24 - 1 workgroups of 2048 / head_dim rows."""
+    most = ((1 << 24) - 1) * (2048 // dim)
+    for tokens, status in ((most, NO_DEVICE), (most + 1, 2), ((1 << 31) - 1, 2)):
+        c, b = structs(dict(c_dim=dim, b_tokens=tokens))
+        for f in (nv.lib().mxfp4_cache_append, nv.lib().mxfp4_cache_read):
+            assert f(c, b, 0x10000, 2 * dim, dim, 0x10000, 2 * dim, dim, None) == status
