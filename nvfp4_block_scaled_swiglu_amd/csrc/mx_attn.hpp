@@ -55,7 +55,8 @@ struct MxAttnPlan {
 // single token's cache with one wave a kv head. Where caches are long a second launch takes
 // the sequences of up to 16 packed rows: 2048 rows over 2048 and 31 single tokens over 8192,
 // 32 heads of 128 over 8, 293 -> 133 us, over 32768 1054 -> 297. Batches without such sequences
-// pay about 8 us for its launches, and over 2048 it saves nothing.
+// pay about 8 us for its launches, and over 2048 it saves nothing. A group of more than 16 heads
+// has no such sequence.
 inline MxAttnPlan mx_attention_plan(int64_t tokens, int64_t batch, int64_t heads, int64_t kv_heads, int64_t head_dim,
                                     int64_t max_kv, int64_t window, int64_t sinks) {
   MxAttnPlan p{true, 1, 1, 0};
@@ -86,7 +87,7 @@ inline MxAttnPlan mx_attention_plan(int64_t tokens, int64_t batch, int64_t heads
   if (s > most_splits) s = most_splits;
   if (s > kMxMostSplits) s = kMxMostSplits;
   p.splits = s < 1 ? 1 : (int)s;
-  if (!p.few && batch > 1 && seen >= 8192) {
+  if (!p.few && batch > 1 && group <= 16 && seen >= 8192) {
     s = 2048 / (batch * kv_heads);
     if (s > seen / (2 * 32 * 4)) s = seen / (2 * 32 * 4);
     if (s > kMxMostSplits) s = kMxMostSplits;

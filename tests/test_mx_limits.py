@@ -53,3 +53,12 @@ def test_rows_of_a_cache_call(no_gpu, dim):
         c, b = structs(dict(c_dim=dim, b_tokens=tokens))
         for f in (nv.lib().mxfp4_cache_append, nv.lib().mxfp4_cache_read):
             assert f(c, b, 0x10000, 2 * dim, dim, 0x10000, 2 * dim, dim, None) == status
+
+
+@pytest.mark.parametrize("group,some", [(16, True), (17, False), (40, False)])
+def test_workspace_of_short_sequences(group, some):
+    """Prompts that need no pieces, long caches: room for sequences of up to 16 rows x heads, which
+    a group of more heads cannot have."""
+    c, b = structs(dict(b_tokens=4000))
+    size = nv.lib().mxfp4_attention_workspace_bytes(c, b, 2 * group, 1 << 14, 0, 0)
+    assert (size > 0) == some
