@@ -125,8 +125,8 @@ typedef struct {
 /*
  * Quantizes new keys and values into the cache at their rows' positions.
  *
- * k_dev, v_dev : bf16 [tokens, kv_heads, head_dim] with strides (elements, multiples of 8)
- *                between tokens and between heads; 16-byte aligned. Read only.
+ * k_dev, v_dev : bf16 [tokens, kv_heads, head_dim] with strides (elements, multiples of 8,
+ *                at most 2^31) between tokens and between heads; 16-byte aligned. Read only.
  * tokens       : at most (2^24 - 1) * 2048 / head_dim, here and in mxfp4_cache_read.
  * Rows without a position (negative, or on a page that is not there) and rows of no
  * sequence are skipped. Nothing else of the cache is touched. Two rows at one place (a page

@@ -183,9 +183,7 @@ def _row_stride(t) -> int:
 def _strides(t) -> Tuple[int, int]:
     """(token, head) strides of [tokens, heads, dim]; those of single ones mean nothing."""
     tokens, heads, dim = t.shape
-    if tokens <= 1:
-        return (heads * dim if heads <= 1 else t.stride(1) * heads, dim if heads <= 1 else t.stride(1))
-    return (t.stride(0), dim if heads <= 1 else t.stride(1))
+    return (t.stride(0) if tokens > 1 else 0, t.stride(1) if heads > 1 else dim)
 
 
 def _current_stream(index: int) -> int:

@@ -48,3 +48,17 @@ def test_many_sequences(gpu):
     out = nv.mxfp4_attention(q, cache, table, seq, cu)
     want = nv.mxfp4_cache_read(cache, table, seq, cu, ROWS)[1]
     assert torch.equal(out, want.repeat_interleave(HEADS // KV_HEADS, 1))
+
+
+def test_one_token_of_heads_first_tensors(gpu):
+    """Query and output as one token of [heads, tokens, dim] tensors; the others stay as they were."""
+    import torch
+    import nvfp4_block_scaled_swiglu_amd as nv
+    from tests.test_gpu_mx_attention import Case
+    c = Case(gpu, [(1, 70)], group=4).fill(gpu)
+    q, out = (torch.full((c.heads, 9, c.dim), 7.0, dtype=torch.bfloat16, device=gpu) for _ in range(2))
+    q[:, 5:6] = c.q.transpose(0, 1)
+    got = nv.mxfp4_attention(q.transpose(0, 1)[5:6], c.cache, c.table, c.seq, c.cu, out=out.transpose(0, 1)[3:4])
+    c.check(got)
+    out[:, 3] = 7.0
+    assert (out == 7.0).all()

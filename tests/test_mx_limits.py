@@ -62,3 +62,18 @@ def test_workspace_of_short_sequences(group, some):
     c, b = structs(dict(b_tokens=4000))
     size = nv.lib().mxfp4_attention_workspace_bytes(c, b, 2 * group, 1 << 14, 0, 0)
     assert (size > 0) == some
+
+
+def test_strides_of_a_single_token(no_gpu):
+    """One token of a heads-first tensor: its stride between tokens means nothing, and must not be
+    made up beyond what is taken (2^31)."""
+    import torch
+    from nvfp4_block_scaled_swiglu_amd import mxfp4
+    x = torch.empty((64, 1 << 20, 64), dtype=torch.bfloat16, device="meta").transpose(0, 1)
+    for t in (x[5:6], x[5:6, :1], x[5:9]):
+        tokens, heads, dim = t.shape
+        strides = mxfp4._strides(t)
+        assert strides[0] == t.stride(0) or tokens == 1
+        assert strides[1] == t.stride(1) or heads == 1
+        c, b = structs(dict(c_heads=heads, b_tokens=tokens))
+        assert nv.lib().mxfp4_cache_read(c, b, 0x10000, *strides, 0x10000, *strides, None) == NO_DEVICE
