@@ -153,9 +153,14 @@ def _buffer(t, name: str, size: int):
     return t
 
 
+_MOST = (1 << 63) - 1  # larger numbers are cut to 64 bits on their way into the library
+
+
 def _packed(t, name: str):
     if not isinstance(t, Mxfp4Tensor):
         raise ValueError(f"{name} must be an Mxfp4Tensor")
+    if t.rows < -_MOST or t.k < -_MOST:  # (if larger than _MOST the buffers are too small)
+        raise ValueError(f"{name}.rows and k must fit 64 bits")
     _buffer(t.qdata, name, t.rows * (t.k // 2))
     _buffer(t.scales, name, _scale_bytes(t.rows, t.k))
     return t
@@ -391,6 +396,11 @@ def mxfp4_cache_read(cache: Mxfp4Cache, block_table, seq_lens, cu_seqlens, token
     return k, v
 
 
+def _limits(max_kv: int, window: int, sinks: int):
+    if not (-_MOST <= max_kv <= _MOST and -_MOST <= window <= _MOST and -_MOST <= sinks <= _MOST):
+        raise ValueError("max_kv, window and sinks must fit 64 bits")
+
+
 def mxfp4_attention(q, cache: Mxfp4Cache, block_table, seq_lens, cu_seqlens, scale: Optional[float] = None,
                     causal: bool = True, window: int = 0, sinks: int = 0, max_kv: Optional[int] = None, out=None,
                     workspace=None, stream=None, strict: Optional[bool] = None):
@@ -414,6 +424,7 @@ def mxfp4_attention(q, cache: Mxfp4Cache, block_table, seq_lens, cu_seqlens, sca
         scale = dim ** -0.5
     if max_kv is None:
         max_kv = max(1, b.max_pages * c.page_size)
+    _limits(max_kv, window, sinks)
     with _On(stream, q, *ct, *bt) as on:
         if out is None:
             out = torch.empty((tokens, heads, dim), dtype=torch.bfloat16, device=on.device)
@@ -440,6 +451,9 @@ def mxfp4_attention_workspace_bytes(cache: Mxfp4Cache, block_table, seq_lens, cu
                                     max_kv: int, window: int = 0, sinks: int = 0) -> int:
     """Bytes of the workspace of a call of these sizes (0: none); raises ValueError where the
     call would be refused."""
+    _limits(max_kv, window, sinks)
+    if not (-_MOST <= tokens <= _MOST and -_MOST <= heads <= _MOST):
+        raise ValueError("tokens and heads must fit 64 bits")
     c, _ = _cache(cache)
     b, _ = _batch(block_table, seq_lens, cu_seqlens, tokens)
     size = int(nv.lib().mxfp4_attention_workspace_bytes(c, b, heads, max_kv, window, sinks))
