@@ -58,7 +58,8 @@ int64_t mxfp4_scale_bytes(int64_t rows, int64_t k);
  * x_dev      : bf16 [rows, k] row-major, row stride ld_x (elements, a multiple of 8, >= k);
  *              16-byte aligned. Read only.
  * rows, k    : rows >= 0 (0: nothing is written, the pointers may be NULL), k > 0,
- *              k % 32 == 0, k and ld_x at most 2^23.
+ *              k % 32 == 0, k and ld_x at most 2^23; ceil(rows / 128) * ceil(k / 512) < 2^21
+ *              (the limits of every [rows, k] below).
  * qdata_dev  : out, mxfp4_qdata_bytes(rows, k) bytes, 16-byte aligned.
  * scales_dev : out, mxfp4_scale_bytes(rows, k) bytes, 16-byte aligned; every byte is
  *              written, padding included.
@@ -84,7 +85,8 @@ int mxfp4_dequantize(const void* qdata_dev, const void* scales_dev, int64_t rows
  * a_*, w_* : matrices [m, k] and [n, k] as mxfp4_quantize writes them.
  * d_dev    : out, bf16 [m, n], row stride ld_d >= n (elements), 2-byte aligned. Rows take
  *            wide stores where d_dev is 16-byte aligned and n and ld_d are multiples of 8.
- * m >= 0 (0: nothing is done), n > 0, k > 0, k % 32 == 0; k at most 2^23.
+ * m >= 0 (0: nothing is done), n > 0, k > 0, k % 32 == 0, both matrices within the limits of
+ * mxfp4_quantize; ceil(m / 64) * ceil(n / 64) < 2^24, ld_d at most 2^40.
  * Every element of D is summed in an order that the sizes alone decide: no atomics, no
  * workspace, no state between calls.
  */
@@ -97,7 +99,8 @@ int mxfp4_gemm_bf16out(const void* a_qdata_dev, const void* a_scales_dev, const 
 /* Keys and values of many sequences in pages of page_size tokens, all in device memory:
  * codes [num_pages, kv_heads, page_size, head_dim / 2] and scales [num_pages, kv_heads,
  * page_size, head_dim / 32], contiguous, 16-byte aligned. head_dim 64, 128 or 256 (blocks
- * run along it); page_size a power of two, 16 to 32768; kv_heads at most 1024. */
+ * run along it); page_size a power of two, 16 to 32768; kv_heads at most 1024, num_pages
+ * below 2^31. */
 typedef struct {
   void* k_codes_dev;
   void* k_scales_dev;
@@ -110,7 +113,8 @@ typedef struct {
  * packed tensors (tokens rows in all, batch + 1 ascending entries from 0); its cache holds
  * seq_lens[b] tokens, of which its rows are the last: row i of n has position
  * seq_lens[b] - n + i. Position p lies in page block_table[b, p / page_size]
- * (int32 [batch, max_pages], row stride table_stride).
+ * (int32 [batch, max_pages], row stride table_stride >= max_pages). batch < 2^24, tokens < 2^31,
+ * max_pages < 2^27, max_pages * page_size < 2^30.
  *
  * seq_lens is clamped to [0, max_pages * page_size] and cu_seqlens to [0, tokens]; a page
  * number outside [0, num_pages) is a page that is not there. Rows past the last sequence
@@ -158,9 +162,10 @@ int64_t mxfp4_attention_workspace_bytes(const mxfp4_cache* cache, const mxfp4_ba
  * nothing gives zeros. A NaN in the cache reaches the rows that see it and no others.
  *
  * q_dev, out_dev : bf16 [tokens, heads, head_dim] with token and head strides (elements,
- *                  multiples of 8); 16-byte aligned. Rows of no sequence are left as they
- *                  were. The rows' own keys and values are in the cache already
- *                  (mxfp4_cache_append with the same batch, before).
+ *                  multiples of 8, at most 2^31); 16-byte aligned. out_dev may be q_dev with
+ *                  the same strides. Rows of no sequence are left as they were. The rows'
+ *                  own keys and values are in the cache already (mxfp4_cache_append with the
+ *                  same batch, before).
  * heads          : a multiple of kv_heads, at most 65536; tokens * heads / kv_heads < 2^31 and
  *                  (tokens * heads / kv_heads / 16 + batch) * kv_heads < 2^24.
  * scale          : > 0, at most 2^127. Scores q . k are fp32 sums and have to lie in its range;
@@ -172,8 +177,10 @@ int64_t mxfp4_attention_workspace_bytes(const mxfp4_cache* cache, const mxfp4_ba
  *                  be NULL if that is 0. Its contents before and after mean nothing. Calls
  *                  that may overlap in time need distinct workspaces.
  * Scores, the softmax and its sums are fp32; weights are rounded to bf16 for their product
- * with the values, and so for their sum. The order of every sum depends on the arguments and
- * lengths alone.
+ * with the values, and so for their sum: against exact weights that moves an element by at most
+ * 2^-8 (sum_t w_t |v_t| + |out|). Sums of weights and values are taken before the division, of
+ * weights up to 2^12: values up to 2^80 in magnitude cannot overflow them. The order of every sum
+ * depends on the arguments and lengths alone.
  */
 int mxfp4_attention(const mxfp4_cache* cache, const mxfp4_batch* batch, const void* q_dev, int64_t q_token_stride,
                     int64_t q_head_stride, int64_t heads, float scale, int causal, int64_t window, int64_t sinks,

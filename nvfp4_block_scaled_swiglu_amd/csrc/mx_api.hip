@@ -3,8 +3,6 @@
 // anything; on an error it returns a status, enqueues nothing and writes nothing.
 #include <hip/hip_runtime.h>
 
-#include <cmath>
-
 #include "api.hpp"
 #include "mx_attn.hpp"
 #include "mxfp4.h"

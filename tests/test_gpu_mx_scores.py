@@ -81,3 +81,15 @@ def test_large_scores_that_rise(gpu, q, kv, scale):
         c.fill(gpu)
         for max_kv in (1, 1 << 14):
             check(c, nv.mxfp4_attention(c.q, c.cache, c.table, c.seq, c.cu, scale=scale, max_kv=max_kv), scale)
+
+
+@pytest.mark.parametrize("exponent", [80, -100])
+@pytest.mark.parametrize("lens", [[(1, 900), (3, 40)], [(60, 700)]])
+def test_values_far_from_one(gpu, lens, exponent):
+    """Values whose weighted sums are near the ends of what fp32 holds."""
+    import nvfp4_block_scaled_swiglu_amd as nv
+    c = Case(gpu, lens, group=3)
+    c.v_bits = mx_ref.f64_to_bits(np.clip(mx_ref.bits_to_f64(c.v_bits) / 8, -1, 1) * 2.0 ** exponent)
+    c.fill(gpu)
+    for max_kv in (1, 1 << 14):
+        c.check(nv.mxfp4_attention(c.q, c.cache, c.table, c.seq, c.cu, max_kv=max_kv))

@@ -77,3 +77,23 @@ def test_strides_of_a_single_token(no_gpu):
         assert strides[1] == t.stride(1) or heads == 1
         c, b = structs(dict(c_heads=heads, b_tokens=tokens))
         assert nv.lib().mxfp4_cache_read(c, b, 0x10000, *strides, 0x10000, *strides, None) == NO_DEVICE
+
+
+@pytest.mark.parametrize("rows,k,status", [
+    (((1 << 21) - 1) * 128, 512, NO_DEVICE), (((1 << 21) - 1) * 128 + 1, 512, 2), (((1 << 21) - 1) * 128, 544, 2),
+    (128, 1 << 23, NO_DEVICE), (127 * 128, 1 << 23, NO_DEVICE), (129 * 128, 1 << 23, 2),
+])
+def test_size_of_a_matrix(no_gpu, rows, k, status):
+    l, p = nv.lib(), 0x10000
+    assert l.mxfp4_quantize(p, k, rows, k, p, p, None) == status
+    assert l.mxfp4_quantize_swiglu(p, k, p, k, rows, k, p, p, None) == status
+    assert l.mxfp4_dequantize(p, p, rows, k, p, k, None) == status
+    assert l.mxfp4_gemm_bf16out(p, p, p, p, p, 64, rows, 64, k, None) == status
+    assert l.mxfp4_gemm_bf16out(p, p, p, p, p, rows, 64, rows, k, None) == status
+
+
+def test_size_of_a_product(no_gpu):
+    f, p = nv.lib().mxfp4_gemm_bf16out, 0x10000
+    assert f(p, p, p, p, p, 1 << 40, 64 << 12, 64 * 4095, 32, None) == NO_DEVICE
+    assert f(p, p, p, p, p, 1 << 40, 64 << 12, 64 * 4096, 32, None) == 2
+    assert f(p, p, p, p, p, (1 << 40) + 1, 64, 64, 32, None) == 2
