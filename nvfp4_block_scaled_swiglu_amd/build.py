@@ -23,9 +23,10 @@ FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=o
 # Per-source additions. The producer's work-queue takes are single-lane atomics whose
 # result is needed one group later; LLVM's atomic optimizer rewrites them into a form
 # that reads the result (and so waits for every load in flight) right after the atomic.
-# The attention kernels work on their scores between two matrix products: with results in
-# ordinary registers (accumulators that only products touch still go to the AGPRs) they need
-# no copies and no spills at one wave a SIMD.
+# The attention kernels work on their scores between two matrix products. With results in
+# ordinary registers (accumulators that only products touch still go to the AGPRs) the prompt
+# form of 256, at one wave a SIMD, spills nothing, otherwise 81 registers (328 bytes a lane);
+# the other forms come out the same either way, those of 64 and 128 with 9 and 8 spilled.
 EXTRA_FLAGS = {"producer.hip": ["-mllvm", "-amdgpu-atomic-optimizer-strategy=None"],
                "mx_attn.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
                "mx_attn_prompt.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}

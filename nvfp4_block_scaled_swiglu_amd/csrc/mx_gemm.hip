@@ -47,8 +47,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // A workgroup of 4 waves (2 x 2) computes (64 FM) x (64 FN), FM = FN = 4 for whole tiles; a
 // wave owns FM x FN tiles of 32 x 32. A stage in LDS holds two K steps of 128: 128 code bytes
 // a row, which a load instruction takes whole from 8 rows, and a KiB of scales per 128 rows.
-// (64 bytes from 16 rows fetch every line twice: 37810 x 5376 x 14336 1,405 us instead of
-// 1,370, 1536 x 5376 x 14336 70.8 instead of 63.5.) Direct-to-LDS loads bring pair ps + kStages while pair
+// (64 bytes from 16 rows fetch every line twice: that took 37810 x 5376 x 14336 from 1,370 to
+// 1,405 us, 1536 x 5376 x 14336 from 63.5 to 70.8.) Direct-to-LDS loads bring pair ps + kStages while pair
 // ps is multiplied.
 // A pair has four quarters of one MFMA per tile each: while the MFMAs of a quarter run, the
 // fragments of the next are read from LDS, in a fixed order of fenced steps (left alone they
@@ -316,7 +316,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void mx_gemm_kernel(MxGemmArgs a) {
 }
 
 // Parts alone, where there is no whole tile: with registers for themselves they need no moves
-// between the two register files, 23.1 -> 20.5 us for 512 x 5376 x 7168, 33.8 -> 29.9 for 1021.
+// between the two register files, 23.1 -> 20.5 us for 512 x 5376 x 7168, 33.8 -> 30 for 1021.
 template <int FM, int FN>
 __global__ __launch_bounds__(64 * kWaves, 2) void mx_gemm_parts_kernel(MxGemmArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
@@ -424,7 +424,8 @@ static_assert(Shape<4, 4>::Lds <= kLds && Shape<2, 2>::Lds <= kLds && kLds <= 16
 // Whole rounds of 256 x 256 tiles, which need the fewest operand bytes a product; in a last
 // round (or the only one) that fills at most half of the CUs, 128 x 256 halves, and 128 x 128
 // quarters where even those fill at most half. Measured at N 5376, K 7168: 168 whole tiles
-// take 48 us, 252 halves 35, 252 quarters 24.
+// take 57 us, 252 halves 38, 252 quarters 23. Parts are counted by tiles, also those without
+// rows: of up to 128 rows half are empty and return at once (48 x 16128 x 5376: 126 of 252).
 hipError_t launch_tiles(MxGemmArgs a, hipStream_t stream) {
   a.tiles_m = (int)((a.m + kEdge - 1) / kEdge);
   a.tiles_n = (int)((a.n + kEdge - 1) / kEdge);
@@ -475,8 +476,8 @@ hipError_t launch_mx_gemm(const uint8_t* aq, const uint8_t* as, const uint8_t* w
   MxGemmArgs a{aq, as, wq, ws, d, ldd, m, n, k, (int)((k / kMxBlock + 3) / 4), 0, 0, 0, 1,
                n % 8 == 0 && ldd % 8 == 0 && ((uintptr_t)d & 15u) == 0};
   // The thin form up to 32 rows, and up to 64 where a wide weight does not give the tiles
-  // enough workgroups: 48 x 5376 x 7168 15.9 us, as tiles 18.2; 48 x 16128 x 5376 18.5 us, as
-  // tiles 15.8; 32 x 5376 x 14336 21.9 us, as tiles 32.1.
+  // enough workgroups: 48 x 5376 x 7168 15.8 us, as tiles 18.0; 48 x 16128 x 5376 22.7 us, as
+  // tiles 14.8; 32 x 5376 x 14336 21.6 us, as tiles 31.6.
   if (m <= 16) return launch_thin<1>(a, stream);
   if (m <= 32) return launch_thin<2>(a, stream);
   if (m <= 64 && n < kThinGroups * 64) return launch_thin<4>(a, stream);
