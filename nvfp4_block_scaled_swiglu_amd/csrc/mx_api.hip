@@ -3,6 +3,9 @@
 // anything; on an error it returns a status, enqueues nothing and writes nothing.
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
+#include <cmath>
+
 #include "api.hpp"
 #include "mx_attn.hpp"
 #include "mxfp4.h"
@@ -304,7 +307,7 @@ int mxfp4_attention(const mxfp4_cache* cache, const mxfp4_batch* batch, const vo
   a.heads = (int)heads;
   a.group = (int)(heads / c.kv_heads);
   a.scale_log2 = scale * 1.44269504f;
-  a.raise = nvfp4::kMxRaise / a.scale_log2;
+  a.raise = fminf(nvfp4::kMxRaise / a.scale_log2, FLT_MAX);
   // lengths stay below 2^30: a window or first tokens beyond that hide nothing more
   a.causal = causal != 0;
   a.window = (int)(window < (1 << 30) ? window : 1 << 30);

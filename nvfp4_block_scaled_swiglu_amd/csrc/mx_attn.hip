@@ -67,13 +67,14 @@ struct Slot {
 constexpr int groups_per_cu(int d, int rt) { return d == 256 ? 2 : rt == 1 ? 4 : 3; }
 constexpr int ring_slots(int d) { return d == 64 ? 4 : 2; }
 
-// LDS of a workgroup: the rings, where the waves' outputs meet afterwards, and their maxima and
-// sums. (Dynamic: of static LDS the compiler knows which object a load into it writes, and
-// waits for all loads in flight before any read of that object.)
+// LDS of a workgroup: the rings, where the waves' outputs meet afterwards, and their references,
+// sums, and exponents of the references' own weights. (Dynamic: of static LDS the compiler knows
+// which object a load into it writes, and waits for all loads in flight before any read of that
+// object.)
 template <int D, int RT>
 struct FewLds {
   static constexpr int Rings = kWaves * ring_slots(D) * Slot<D>::Bytes, Red = kWaves * (D / 4) * 64 * 4;
-  static constexpr int Ring = Rings > Red ? Rings : Red, Bytes = Ring + 2 * kWaves * RT * 16 * 4;
+  static constexpr int Ring = Rings > Red ? Rings : Red, Bytes = Ring + 3 * kWaves * RT * 16 * 4;
 };
 
 template <int N>
@@ -132,15 +133,15 @@ __global__ __launch_bounds__(64 * kWaves, groups_per_cu(D, RT)) void mx_attentio
   // 64 entries of the block table at a time, one a lane
   const int32_t* table = a.b.block_table + (int64_t)rows.seq * a.b.table_stride;
   const int pages = (rows.kv_len + (1 << a.b.page_shift) - 1) >> a.b.page_shift;
-  int entry = -1, base = -64;
+  int entry = -1, held = -64;
   auto page_of = [&](int t) __attribute__((always_inline)) -> int {
     const int p = t >> a.b.page_shift;
-    if (p < base || p >= base + 64) {  // uniform
-      base = p;
+    if (p < held || p >= held + 64) {  // uniform
+      held = p;
       entry = p + lane < pages ? table[p + lane] : -1;
       if (entry >= a.b.num_pages) entry = -1;
     }
-    return __builtin_amdgcn_readlane(entry, p - base);
+    return __builtin_amdgcn_readlane(entry, p - held);
   };
   uint8_t* const ring = smem + wave * (R * S::Bytes);
   const bool halves = a.b.page_shift == 4;  // else the halves of a tile share a page
@@ -193,12 +194,12 @@ __global__ __launch_bounds__(64 * kWaves, groups_per_cu(D, RT)) void mx_attentio
   // ---- state ----
   f32x4_t o[RT][NJ];
   float m[RT], l[RT];       // m: the reference score, agreed by the four lanes of a row; l: the lane's own tokens
-  float neg[RT], most[RT];  // of its unit; the score up to which it stays
-  bool far = false;         // some row's reference is
+  float base[RT], neg[RT];  // its unit
+  float most[RT];           // the score up to which it stays
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
     m[r] = most[r] = -INFINITY;
-    l[r] = neg[r] = 0.0f;
+    l[r] = base[r] = neg[r] = 0.0f;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) o[r][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   }
@@ -243,18 +244,18 @@ __global__ __launch_bounds__(64 * kWaves, groups_per_cu(D, RT)) void mx_attentio
     for (int r = 0; r < RT; ++r) {
       float top = fmaxf(fmaxf(fmaxf(s[r][0][0], s[r][0][1]), fmaxf(s[r][0][2], s[r][0][3])),
                         fmaxf(fmaxf(s[r][1][0], s[r][1][1]), fmaxf(s[r][1][2], s[r][1][3])));
-      if (far | __any(!(top <= most[r]))) {
+      if (__any(top > most[r])) {
         top = fmaxf(top, __shfl_xor(top, 16, 64));
         top = fmaxf(top, __shfl_xor(top, 32, 64));
         const float next = fmaxf(m[r], top);
         const MxUnit unit = mx_unit(a, next);
-        far |= __any(unit.far);
-        const float f = mx_rebase(a, m[r], next);  // m = -inf: o and l are 0
+        // mx_rebase with the units at hand, without a branch; m = -inf: o and l are 0
+        const float e = mx_exponent(a, m[r], unit.base, unit.neg) - mx_exponent(a, m[r], base[r], neg[r]);
+        const float f = m[r] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(e);
         m[r] = next;
+        base[r] = unit.base;
         neg[r] = unit.neg;
-        most[r] = next == -INFINITY ? -INFINITY : next + a.raise;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) s[r][h] -= unit.base;  // 0 unless far, when every step comes here
+        most[r] = next + a.raise;
         l[r] *= f;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) o[r][j] *= f;
@@ -262,7 +263,7 @@ __global__ __launch_bounds__(64 * kWaves, groups_per_cu(D, RT)) void mx_attentio
       float p[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        p[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][j >> 2][j & 3], a.scale_log2, neg[r]));
+        p[j] = __builtin_amdgcn_exp2f(mx_exponent(a, s[r][j >> 2][j & 3], base[r], neg[r]));
       uint32_t w[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -371,6 +372,8 @@ __global__ __launch_bounds__(64 * kWaves, groups_per_cu(D, RT)) void mx_attentio
     if (u == 0) {
       ml[(wave * RT + r) * 16 + n] = m[r];
       ml[(kWaves * RT + wave * RT + r) * 16 + n] = l[r];
+      ml[(2 * kWaves * RT + wave * RT + r) * 16 + n] =
+          m[r] == -INFINITY ? 0.0f : mx_exponent(a, m[r], base[r], neg[r]);  // 0: its f is 2^-inf
     }
   }
 #pragma unroll
@@ -379,10 +382,11 @@ __global__ __launch_bounds__(64 * kWaves, groups_per_cu(D, RT)) void mx_attentio
     float top = -INFINITY, sum = 0.0f, f[kWaves];
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) top = fmaxf(top, ml[(w * RT + r) * 16 + n]);
+    const MxUnit unit = mx_unit(a, top);
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
       const float mw = ml[(w * RT + r) * 16 + n];
-      f[w] = mx_rebase(a, mw, top);
+      f[w] = __builtin_amdgcn_exp2f(mx_exponent(a, mw, unit.base, unit.neg) - ml[(2 * kWaves * RT + w * RT + r) * 16 + n]);
       sum += f[w] * ml[(kWaves * RT + w * RT + r) * 16 + n];
     }
 #pragma unroll

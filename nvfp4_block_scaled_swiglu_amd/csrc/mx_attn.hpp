@@ -133,15 +133,20 @@ __device__ __forceinline__ MxUnit mx_unit(const MxAttnArgs& a, float t) {
   return MxUnit{far ? t : 0.0f, far || none ? 0.0f : -e, far};
 }
 
-// What weights and their sums under reference t are multiplied with to be under reference u >= t;
-// 1 if there are none. (A quick way out where no lane is far costs more than it saves: the prompt
-// form of 64 then spills, 99 us for 91.)
+// of the weight of score x
+__device__ __forceinline__ float mx_exponent(const MxAttnArgs& a, float x, float base, float neg) {
+  return __builtin_fmaf(x - base, a.scale_log2, neg);
+}
+
+// What weights and their sums under reference t are multiplied with to be under reference u >= t
+// (anything if there are none): t's own weight is 2^off, and becomes that under u's unit. (The
+// early way out matters: without it the prompt form of 64 spills, 99 us for 91.)
 __device__ __forceinline__ float mx_rebase(const MxAttnArgs& a, float t, float u) {
   const MxUnit from = mx_unit(a, t);
-  const float off = from.far ? 0.0f : __builtin_fmaf(t, a.scale_log2, from.neg);  // of t from its unit
+  const float off = mx_exponent(a, t, from.base, from.neg);
   if (t == u || t == -INFINITY) return 1.0f;
   const MxUnit to = mx_unit(a, u);
-  return __builtin_amdgcn_exp2f(__builtin_fmaf(t - to.base, a.scale_log2, to.neg) - off);
+  return __builtin_amdgcn_exp2f(mx_exponent(a, t, to.base, to.neg) - off);
 }
 
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8_t;
