@@ -13,7 +13,7 @@
 // element. A wave moves its codes and scales to a ring of its own in LDS, 32 tokens a slot,
 // with direct-to-LDS loads that need no register while they fly and no barrier (six
 // instructions for 32 tokens of 128 elements, every one of whole runs): 16 waves x 2 slots
-// x 4.25 KiB in flight per CU. 48 single tokens over up to 8200, 56 heads of 128 over 8: 78
+// x 4.25 KiB in flight per CU. 48 single tokens over up to 8200, 56 heads of 128 over 8: 77
 // us and 5 of joining, 4.2 TB/s of the cache; the loads alone take 63, the rest alone 69.
 //
 // One pass with the running maximum and sum of the softmax, in the transposed form with
