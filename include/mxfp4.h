@@ -187,6 +187,182 @@ int mxfp4_attention(const mxfp4_cache* cache, const mxfp4_batch* batch, const vo
                     int64_t max_kv, void* out_dev, int64_t out_token_stride, int64_t out_head_stride,
                     void* workspace_dev, int64_t workspace_bytes, void* stream);
 
+/* ---- attention behind shared prefixes ---------------------------------------------------- */
+
+/* Groups of consecutive sequences that begin with the same tokens (answers to one prompt,
+ * questions behind one set of instructions). Group g has the sequences group_starts[g] ..
+ * group_starts[g + 1] - 1 of the batch (groups + 1 ascending entries; sequences before the first
+ * and from the last on are in no group); its prefix is the lens[g] tokens in the pages of row g
+ * of its block table (int32 [groups, max_pages], row stride table_stride >= max_pages), of which the first
+ * lens[g] / 64 * 64 are shared. groups < 2^24, max_pages < 2^27, max_pages * page_size < 2^30.
+ * lens is clamped to [0, max_pages * page_size] and group_starts to [0, batch]. */
+typedef struct {
+  const int32_t* block_table_dev;
+  const int32_t* lens_dev;
+  const int32_t* group_starts_dev;
+  int64_t groups, max_pages, table_stride;
+} mxfp4_prefix;
+
+/* Bytes of mxfp4_attention_prefix's workspace for a call of these sizes; -1 for arguments that
+ * the call itself refuses. */
+int64_t mxfp4_attention_prefix_workspace_bytes(const mxfp4_cache* cache, const mxfp4_batch* batch,
+                                               const mxfp4_prefix* prefix, int64_t heads, int64_t max_prefix,
+                                               int64_t max_own);
+
+/*
+ * mxfp4_attention without a window, where a sequence's shared tokens are read through its
+ * group's block table and only the others through its own row of the batch's: the cached prefix is
+ * read once for all rows of a group. Of a sequence whose first row does not see all of the shared
+ * tokens (with causal: its position + 1 is smaller than their number; without: its length is), and of
+ * one in no group, all tokens are read through its own row.
+ *
+ * A sequence's own row is not read below the shared tokens; above them a page that holds the first of its
+ * own tokens is its own.
+ * max_prefix, max_own : the longest prefix, and the most tokens of a sequence behind its own, as
+ *                       far as the caller knows (> 0). They only decide how the work is split.
+ * The rest as in mxfp4_attention; tokens * heads < 2^26.
+ */
+int mxfp4_attention_prefix(const mxfp4_cache* cache, const mxfp4_batch* batch, const mxfp4_prefix* prefix,
+                           const void* q_dev, int64_t q_token_stride, int64_t q_head_stride, int64_t heads, float scale,
+                           int causal, int64_t max_prefix, int64_t max_own, void* out_dev, int64_t out_token_stride,
+                           int64_t out_head_stride, void* workspace_dev, int64_t workspace_bytes, void* stream);
+
+/* ---- norms and rotation of heads --------------------------------------------------------- */
+
+/* n = x w / sqrt(mean(x^2) + eps) over the head_dim elements of a head. weight_dev: bf16
+ * [head_dim], 16-byte aligned, or NULL for ones; eps > 0 and finite. */
+typedef struct {
+  const void* weight_dev;
+  double eps;
+} mxfp4_norm;
+
+/* Rotation of the first rotary_dim elements of a head by pairs: (a, b) becomes
+ * (a cos t - b sin t, b cos t + a sin t), t = position * freqs[j]. Pair j is (j, j + rotary_dim / 2),
+ * with interleaved != 0 (2 j, 2 j + 1).
+ *
+ * rotary_dim    : a multiple of 16, 16 to head_dim.
+ * freqs_dev     : fp32 [rotary_dim / 2], finite, 4-byte aligned.
+ * axes_dev      : int32 [rotary_dim / 2], which of a row's positions turns the pair (of
+ *                 time, height and width, say), clamped to [0, axes); NULL: axis 0.
+ * positions_dev : int32, that of row i on axis x at [i * token_stride + x * axis_stride] (elements,
+ *                 0 to 2^31); NULL in a call with a cache: the row's position in its sequence, on every axis.
+ * axes          : 1 to 64.
+ * Angles are taken in fp64 for every position, whatever its size. */
+typedef struct {
+  const float* freqs_dev;
+  const int32_t* axes_dev;
+  const int32_t* positions_dev;
+  int64_t rotary_dim, axes, token_stride, axis_stride;
+  int interleaved;
+} mxfp4_rotation;
+
+/*
+ * out[i, h] = RN_bf16(rotation(norm(x[i, h]))), in one launch that reads x once.
+ *
+ * x_dev, out_dev : bf16 [tokens, heads, head_dim] with token and head strides (elements,
+ *                  multiples of 8, at most 2^31); 16-byte aligned. out_dev may be x_dev with the
+ *                  same strides. head_dim 64, 128 or 256; heads 1 to 65536; tokens < 2^26.
+ * norm, rotation : each may be NULL (left out).
+ * Sums and products are fp32 (fp64 for heads whose squares leave its range). A head with an
+ * infinity or a NaN comes out as the formulas have it.
+ */
+int mxfp4_norm_rope(const void* x_dev, int64_t x_token_stride, int64_t x_head_stride, int64_t tokens, int64_t heads,
+                    int64_t head_dim, const mxfp4_norm* norm, const mxfp4_rotation* rotation, void* out_dev,
+                    int64_t out_token_stride, int64_t out_head_stride, void* stream);
+
+/*
+ * What stands between a QKV projection and mxfp4_attention, in one launch: q as mxfp4_norm_rope
+ * writes it (q_norm); k likewise (k_norm), its bf16 values then quantized into the cache; v
+ * quantized into the cache as it is. Places are those of mxfp4_cache_append, whose rules for
+ * rows hold: rows of no sequence are left out (and their q as it was), a row without a place
+ * leaves the cache as it is, and its q is written.
+ *
+ * q_dev, q_out_dev : bf16 [tokens, heads, head_dim]; with heads == 0 none (NULL). The row's
+ *                    head_dim and kv_heads are the cache's.
+ * k_dev, v_dev     : bf16 [tokens, kv_heads, head_dim].
+ * Norm and rotation of k are fp64 throughout: a last bit decides the way to 4 bits.
+ */
+int mxfp4_norm_rope_append(const mxfp4_cache* cache, const mxfp4_batch* batch, const void* q_dev, int64_t q_token_stride,
+                           int64_t q_head_stride, int64_t heads, const mxfp4_norm* q_norm, const void* k_dev,
+                           int64_t k_token_stride, int64_t k_head_stride, const mxfp4_norm* k_norm, const void* v_dev,
+                           int64_t v_token_stride, int64_t v_head_stride, const mxfp4_rotation* rotation,
+                           void* q_out_dev, int64_t out_token_stride, int64_t out_head_stride, void* stream);
+
+/* ---- pages --------------------------------------------------------------------------------- */
+
+/* Which pages the sequences of a cache hold, all in device memory. A sequence is a slot: row
+ * s of the block table (int32 [slots, max_pages], row stride table_stride >= max_pages) and its length
+ * seq_lens[s], which is clamped to [0, max_pages * page_size]. It holds the first
+ * ceil(length / page_size) entries. refs[p] (int32 [num_pages]) is how many entries
+ * hold page p; a page whose count is below 1 is free. slots < 2^24, num_pages < 2^31, the rest as in
+ * mxfp4_batch. Page numbers outside [0, num_pages) count as no page. Several caches (the
+ * layers of a model) can go by one such record.
+ *
+ * Lists of slots are int32 in device memory, n < 65536 entries; entries outside [0, slots) are passed
+ * over. Results do not depend on timing. done_dev says for each entry whether it was
+ * carried out (1) or left everything as it was (0). */
+typedef struct {
+  int32_t* block_table_dev;
+  int32_t* seq_lens_dev;
+  int32_t* refs_dev;
+  int64_t slots, max_pages, table_stride, num_pages, page_size;
+} mxfp4_pages;
+
+/* Cuts each listed sequence back to keep_dev[i] tokens (NULL: none) if it is longer; pages
+ * behind them are given back, their entries become -1. A slot that is listed twice keeps the
+ * smaller number. */
+int mxfp4_pages_free(const mxfp4_pages* pages, const int32_t* slots_dev, const int32_t* keep_dev, int64_t n,
+                     void* stream);
+
+/* Makes slot children_dev[i] a copy of the sequence in parents_dev[i], which then share their
+ * pages, a last one that is not full among them. Not done where the child's length is not 0,
+ * where an earlier entry has the same child, and where the parent is itself a child in the list. */
+int mxfp4_pages_fork(const mxfp4_pages* pages, const int32_t* parents_dev, const int32_t* children_dev, int64_t n,
+                     int32_t* done_dev, void* stream);
+
+/* Bytes of mxfp4_pages_reserve's workspace; -1 for arguments that the call itself refuses. */
+int64_t mxfp4_pages_reserve_workspace_bytes(const mxfp4_pages* pages, int64_t n);
+
+/*
+ * Lengthens sequence slots_dev[i] to lens_dev[i] tokens, with new pages for them. A last page that is
+ * not full and that other entries hold too is replaced: src_dev[i] is the page, dst_dev[i] the
+ * new one, into which mxfp4_cache_copy has to copy it in every cache before its next token is written and before
+ * pages are given out again; both are -1 where there is none.
+ *
+ * Pages are given out lowest first, in the list's order. Not done where the length is below the
+ * present one or beyond max_pages * page_size, where an earlier entry has the same slot, and where the
+ * need of the entries up to it (served or not) is more than the pages that were free.
+ * workspace_dev: 16-byte aligned, mxfp4_pages_reserve_workspace_bytes bytes.
+ */
+int mxfp4_pages_reserve(const mxfp4_pages* pages, const int32_t* slots_dev, const int32_t* lens_dev, int64_t n,
+                        int32_t* done_dev, int32_t* src_dev, int32_t* dst_dev, void* workspace_dev,
+                        int64_t workspace_bytes, void* stream);
+
+/* Bytes of mxfp4_pages_compact's workspace; -1 for arguments that the call itself refuses. */
+int64_t mxfp4_pages_compact_workspace_bytes(const mxfp4_pages* pages);
+
+/*
+ * Numbers the used pages so that they are the first ones: with u in use, those at u and above move, in order, into
+ * the free ones below u. Page src_dev[k] becomes dst_dev[k] (int32 [num_pages / 2] each,
+ * ascending, -1 behind the last), used_dev[0] = u. The new block table and counts go to table_out_dev
+ * (row stride table_out_stride >= max_pages) and refs_out_dev, which may be those of `pages`: with buffers
+ * of their own the old ones stay in use until mxfp4_cache_copy has moved the pages, which
+ * it does not disturb. workspace_dev: 16-byte aligned.
+ * ceil(num_pages / 256) + slots * ceil(max_pages / 256) < 2^24.
+ */
+int mxfp4_pages_compact(const mxfp4_pages* pages, int32_t* table_out_dev, int64_t table_out_stride, int32_t* refs_out_dev,
+                        int32_t* src_dev, int32_t* dst_dev, int32_t* used_dev, void* workspace_dev,
+                        int64_t workspace_bytes, void* stream);
+
+/*
+ * Copies whole pages of keys and values, src_dev[i] of `from` to dst_dev[i] of `to` (int32 [n], n < 2^31),
+ * which may be one cache and differ in num_pages at most. A pair with a page out of range moves
+ * nothing. A page that is written by two pairs, or read by one and written by another,
+ * leaves what is written undefined.
+ */
+int mxfp4_cache_copy(const mxfp4_cache* from, const mxfp4_cache* to, const int32_t* src_dev, const int32_t* dst_dev,
+                     int64_t n, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -16,7 +16,8 @@ Functions carry the C names:
 * ``nvfp4_gemm_bf16out(a, w)``        - block-scaled GEMM, FP32 accumulation, BF16 out
 * ``nvfp4_silu_bf16(x)``              - the producer's bf16 silu, elementwise (self-test)
 * size helpers ``nvfp4_padded_rows``, ``nvfp4_qdata_bytes``, ``nvfp4_scale_bytes``, ...
-* the MXFP4 operators (``mxfp4_*``: quantization, product, paged cache, attention) of ``mxfp4.py``
+* the MXFP4 operators (``mxfp4_*``) of ``mxfp4.py`` (quantization, product, paged cache, attention),
+  ``mxfp4_rope.py`` (head norms and rotation) and ``mxfp4_pages.py`` (the cache's pages)
 """
 from __future__ import annotations
 
@@ -495,6 +496,11 @@ def nvfp4_silu_bf16(x, out=None, stream=None):
 
 
 from .mxfp4 import (  # noqa: E402  (the operators use the names above)
-    Mxfp4Cache, Mxfp4Tensor, empty_mxfp4, empty_mxfp4_cache, mxfp4_attention, mxfp4_attention_workspace_bytes,
-    mxfp4_cache_append, mxfp4_cache_read, mxfp4_dequantize, mxfp4_gemm_bf16out, mxfp4_qdata_bytes, mxfp4_quantize,
-    mxfp4_quantize_swiglu, mxfp4_scale_bytes, mxfp4_scale_cols)
+    Mxfp4Cache, Mxfp4Tensor, empty_mxfp4, empty_mxfp4_cache, mxfp4_attention, mxfp4_attention_prefix,
+    mxfp4_attention_prefix_workspace_bytes, mxfp4_attention_workspace_bytes, mxfp4_cache_append, mxfp4_cache_read,
+    mxfp4_dequantize, mxfp4_gemm_bf16out, mxfp4_qdata_bytes, mxfp4_quantize, mxfp4_quantize_swiglu, mxfp4_scale_bytes,
+    mxfp4_scale_cols)
+from .mxfp4_pages import (  # noqa: E402
+    Mxfp4Pages, empty_mxfp4_pages, mxfp4_cache_copy, mxfp4_pages_compact, mxfp4_pages_compact_workspace_bytes,
+    mxfp4_pages_fork, mxfp4_pages_free, mxfp4_pages_reserve, mxfp4_pages_reserve_workspace_bytes)
+from .mxfp4_rope import Mxfp4Rotation, mxfp4_norm_rope, mxfp4_norm_rope_append, mxfp4_rotation  # noqa: E402

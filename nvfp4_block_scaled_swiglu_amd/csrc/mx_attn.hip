@@ -84,7 +84,7 @@ __device__ __forceinline__ void wait_loads() {  // vmcnt(N)
   asm volatile("" ::: "memory");
 }
 
-template <int D, int RT>
+template <int D, int RT, MxPart PART>
 __global__ __launch_bounds__(64 * kWaves, groups_per_cu(D, RT)) void mx_attention_few_kernel(MxAttnArgs a) {
   using S = Slot<D>;
   constexpr int NJ = D / 16, KS = D / 32, E = D / 4, R = ring_slots(D);
@@ -100,9 +100,10 @@ __global__ __launch_bounds__(64 * kWaves, groups_per_cu(D, RT)) void mx_attentio
   const int g = a.group;
   // the longest contexts are not known here; the last tiles come first, as in the prompt form
   const int tile = (gridDim.x - 1 - blockIdx.x) / a.c.kv_heads;
-  const MxRows rows = a.by_seq ? mx_rows_of(a, tile) : mx_rows(a, tile, kRows);
+  const bool by_seq = PART == kMxWhole && a.by_seq;
+  const MxRows rows = by_seq ? mx_rows_of(a, tile) : mx_rows<PART>(a, tile, kRows);
   const int p0 = rows.first;
-  if (p0 >= rows.count || (a.by_seq && rows.count > kRows)) return;  // the whole workgroup
+  if (p0 >= rows.count || (by_seq && rows.count > kRows)) return;  // the whole workgroup
   const int p1 = p0 + kRows < rows.count ? p0 + kRows : rows.count;
 
   // ---- the rows ----
@@ -120,10 +121,10 @@ __global__ __launch_bounds__(64 * kWaves, groups_per_cu(D, RT)) void mx_attentio
       if (real) w = *(const u32x4_t*)(src + 8 * s);
       q[r][s] = as_bf16x8(w[0], w[1], w[2], w[3]);
     }
-    high[r] = real ? mx_high(a, rows.kv_len, rows.back + i) : 0;
-    low[r] = mx_low(a, rows.back + i);
+    high[r] = real ? mx_row_high<PART>(a, rows, i) : 0;
+    low[r] = mx_row_low<PART>(a, rows, i);
   }
-  const MxSight sight = mx_sight(a, rows, p0, p1);
+  const MxSight sight = mx_sight<PART>(a, rows, p0, p1);
   const int high_min = p1 - p0 < kRows ? 0 : sight.high_min;  // rows that are not there see nothing
   const MxSpan span = mx_span(sight, kTile);
   const int from = mx_share(span.count, split, a.splits), to = mx_share(span.count, split + 1, a.splits);
@@ -131,7 +132,7 @@ __global__ __launch_bounds__(64 * kWaves, groups_per_cu(D, RT)) void mx_attentio
 
   // ---- loads ----
   // 64 entries of the block table at a time, one a lane
-  const int32_t* table = a.b.block_table + (int64_t)rows.seq * a.b.table_stride;
+  const int32_t* table = mx_table<PART>(a, rows);
   const int pages = (rows.kv_len + (1 << a.b.page_shift) - 1) >> a.b.page_shift;
   int entry = -1, held = -64;
   auto page_of = [&](int t) __attribute__((always_inline)) -> int {
@@ -406,8 +407,10 @@ __global__ __launch_bounds__(64 * kWaves, groups_per_cu(D, RT)) void mx_attentio
     const int64_t token = rows.r0 + p / g;
     const int head = kvh * g + p % g;
     const int e0 = (4 * u + wave) * NJ;
-    if (a.splits > 1) {
-      const int64_t at = a.by_seq ? (((int64_t)split * a.b.batch + rows.seq) * a.c.kv_heads + kvh) * 16 + n
+    if (PART != kMxWhole || a.splits > 1) {
+      if (PART == kMxOwn && !rows.shared && split == 0 && u == 0 && wave == 0)
+        mx_drop_prefix(a, token, head);
+      const int64_t at = by_seq ? (((int64_t)split * a.b.batch + rows.seq) * a.c.kv_heads + kvh) * 16 + n
                                   : ((int64_t)split * a.b.tokens + token) * a.heads + head;
       if (u == 0 && wave == 0) a.part_ml[at] = make_float2(top, sum);
       if (sum != 0.0f) {
@@ -551,10 +554,11 @@ __global__ __launch_bounds__(256) void mx_attention_join_kernel(MxAttnArgs a) {
       u32x2_t{pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv)};
 }
 
-template <int D, int RT>
+template <int D, int RT, MxPart PART = kMxWhole>
 hipError_t launch_few(const MxAttnArgs& a, hipStream_t stream) {
-  const int64_t tiles = a.by_seq ? a.b.batch : a.b.tokens * a.group / (16 * RT) + a.b.batch;
-  mx_attention_few_kernel<D, RT>
+  const int64_t tiles = a.by_seq ? a.b.batch
+                                 : a.b.tokens * a.group / (16 * RT) + (PART == kMxPrefix ? a.prefix.groups : a.b.batch);
+  mx_attention_few_kernel<D, RT, PART>
       <<<dim3((unsigned)(tiles * a.c.kv_heads), a.splits), 64 * kWaves, FewLds<D, RT>::Bytes, stream>>>(a);
   return hipGetLastError();
 }
@@ -586,7 +590,7 @@ hipError_t launch_dim(MxAttnArgs a, const MxAttnPlan& plan, hipStream_t stream) 
     e = launch_few<D, 1>(few, stream);
     if (e != hipSuccess) return e;
   }
-  e = launch_mx_attention_prompt(a, stream);
+  e = launch_mx_attention_prompt(a, kMxWhole, stream);
   // Of the few-rows form's sequences the first join writes what nobody left for it; where
   // there is one (few groups, long caches) those are in pieces too, and the second is right.
   if (e == hipSuccess) e = join<D>(a, stream);
@@ -594,19 +598,54 @@ hipError_t launch_dim(MxAttnArgs a, const MxAttnPlan& plan, hipStream_t stream) 
   return e;
 }
 
-template <int D, int RT>
+// a group's prefix, or what is left of the sequences, into pieces
+template <int D, MxPart PART>
+hipError_t launch_part(const MxAttnArgs& a, const MxAttnPlan& plan, hipStream_t stream) {
+  if (!plan.few) return launch_mx_attention_prompt(a, PART, stream);
+  if (plan.row_tiles == 1) return launch_few<D, 1, PART>(a, stream);
+  return launch_few<D, D == 64 ? 2 : 1, PART>(a, stream);
+}
+
+template <int D>
+hipError_t launch_prefix_dim(const MxAttnArgs& a, const MxPrefixPlan& plan, hipStream_t stream) {
+  const int64_t rows = a.b.tokens * a.heads;
+  const int pieces = plan.prefix.splits + plan.own.splits;
+  MxAttnArgs x = a;
+  x.part_ml = (float2*)(a.part_o + pieces * rows * D);
+  x.splits = plan.prefix.splits;
+  MxAttnArgs y = x;
+  y.prefix_ml = x.part_ml;
+  y.prefix_splits = x.splits;
+  y.part_o += x.splits * rows * D;
+  y.part_ml += x.splits * rows;
+  y.splits = plan.own.splits;
+  hipError_t e = launch_part<D, kMxPrefix>(x, plan.prefix, stream);
+  if (e == hipSuccess) e = launch_part<D, kMxOwn>(y, plan.own, stream);
+  x.splits = pieces;
+  return e == hipSuccess ? join<D>(x, stream) : e;
+}
+
+template <int D, int RT, MxPart PART = kMxWhole>
 hipError_t setup_few() {
-  return hipFuncSetAttribute((const void*)mx_attention_few_kernel<D, RT>, hipFuncAttributeMaxDynamicSharedMemorySize,
+  return hipFuncSetAttribute((const void*)mx_attention_few_kernel<D, RT, PART>, hipFuncAttributeMaxDynamicSharedMemorySize,
                              FewLds<D, RT>::Bytes);
+}
+
+template <int D, int RT>
+hipError_t setup_parts() {
+  hipError_t e = setup_few<D, RT>();
+  if (e == hipSuccess) e = setup_few<D, RT, kMxPrefix>();
+  if (e == hipSuccess) e = setup_few<D, RT, kMxOwn>();
+  return e;
 }
 
 }  // namespace
 
 hipError_t mx_attention_setup() {
-  hipError_t e = setup_few<64, 1>();
-  if (e == hipSuccess) e = setup_few<64, 2>();
-  if (e == hipSuccess) e = setup_few<128, 1>();
-  if (e == hipSuccess) e = setup_few<256, 1>();
+  hipError_t e = setup_parts<64, 1>();
+  if (e == hipSuccess) e = setup_parts<64, 2>();
+  if (e == hipSuccess) e = setup_parts<128, 1>();
+  if (e == hipSuccess) e = setup_parts<256, 1>();
   if (e == hipSuccess) e = mx_attention_prompt_setup();
   return e;
 }
@@ -616,6 +655,14 @@ hipError_t launch_mx_attention(const MxAttnArgs& a, const MxAttnPlan& plan, hipS
     case 64: return launch_dim<64>(a, plan, stream);
     case 128: return launch_dim<128>(a, plan, stream);
     default: return launch_dim<256>(a, plan, stream);
+  }
+}
+
+hipError_t launch_mx_attention_prefix(const MxAttnArgs& a, const MxPrefixPlan& plan, hipStream_t stream) {
+  switch (a.c.head_dim) {
+    case 64: return launch_prefix_dim<64>(a, plan, stream);
+    case 128: return launch_prefix_dim<128>(a, plan, stream);
+    default: return launch_prefix_dim<256>(a, plan, stream);
   }
 }
 

@@ -5,6 +5,22 @@
 
 namespace nvfp4 {
 
+// Groups of consecutive sequences whose first tokens are read through one block table: the
+// whole kMxShared of them that every row of a sequence sees.
+struct MxPrefix {
+  const int32_t* block_table;  // [groups, max_pages]
+  const int32_t* lens;         // [groups]
+  const int32_t* starts;       // [groups + 1] first sequence of each group
+  int64_t table_stride;
+  int groups, max_pages;
+};
+
+constexpr int kMxShared = 64;  // tokens: whole tiles of either form
+
+// Which tokens a launch is for: all that its rows see, a group's prefix for the rows of all of
+// its sequences, or what is left of each sequence.
+enum MxPart { kMxWhole, kMxPrefix, kMxOwn };
+
 struct MxAttnArgs {
   MxBatch b;
   MxCache c;
@@ -19,9 +35,12 @@ struct MxAttnArgs {
   float2* part_ml;  // [splits, tokens, heads] reference score and sum; by_seq likewise
   int skip;         // prompt form: sequences of up to so many packed rows are not its own
   bool by_seq;      // few-rows form: a workgroup a sequence and kv head, of up to 16 packed rows
+  MxPrefix prefix;  // kMxPrefix and kMxOwn, whose launches always leave pieces
+  float2* prefix_ml;      // kMxOwn: the prefix's pieces, [prefix_splits, tokens, heads]
+  int prefix_splits;
 };
 
-constexpr int kMxMostSplits = 256;
+constexpr int kMxMostSplits = 256;  // that a join takes
 
 // How a call is cut, from its sizes alone.
 struct MxAttnPlan {
@@ -107,8 +126,28 @@ inline int64_t mx_part_bytes(const MxAttnPlan& p, int64_t tokens, int64_t batch,
          (p.mixed > 1 ? p.mixed * batch * kv_heads * 16 * (head_dim + 2) * 4 : 0);
 }
 
+// A call with shared prefixes: what the groups' rows see of them, and the rest of the sequences.
+struct MxPrefixPlan {
+  MxAttnPlan prefix, own;
+};
+
+inline MxPrefixPlan mx_prefix_plan(int64_t tokens, int64_t batch, int64_t groups, int64_t heads, int64_t kv_heads,
+                                   int64_t head_dim, int64_t max_prefix, int64_t max_own) {
+  MxPrefixPlan p;
+  p.prefix = mx_attention_plan(tokens, groups < tokens ? groups : tokens, heads, kv_heads, head_dim, max_prefix, 0, 0);
+  p.own = mx_attention_plan(tokens, batch, heads, kv_heads, head_dim, max_own, 0, 0);
+  p.prefix.mixed = p.own.mixed = 0;
+  if (p.prefix.splits > kMxMostSplits / 2) p.prefix.splits = kMxMostSplits / 2;
+  if (p.own.splits > kMxMostSplits / 2) p.own.splits = kMxMostSplits / 2;
+  return p;
+}
+
+inline int64_t mx_prefix_bytes(const MxPrefixPlan& p, int64_t tokens, int64_t heads, int64_t head_dim) {
+  return ((p.prefix.splits + p.own.splits) * tokens * heads * (head_dim + 2) * 4 + 15) / 16 * 16;
+}
+
 hipError_t mx_attention_prompt_setup();
-hipError_t launch_mx_attention_prompt(const MxAttnArgs& a, hipStream_t stream);
+hipError_t launch_mx_attention_prompt(const MxAttnArgs& a, MxPart part, hipStream_t stream);
 
 // ---- device side ----
 
@@ -176,6 +215,12 @@ __device__ __forceinline__ uint32_t decode2(uint32_t q, float s, int sel) {
   }
 }
 
+// a row that reads all of its tokens itself: the prefix's pieces of its group are not its own
+__device__ __forceinline__ void mx_drop_prefix(const MxAttnArgs& a, int64_t token, int head) {
+  for (int s = 0; s < a.prefix_splits; ++s)
+    a.prefix_ml[((int64_t)s * a.b.tokens + token) * a.heads + head] = make_float2(-INFINITY, 0.0f);
+}
+
 // bits -> eight bf16 that are 1 where the bit is set
 __device__ __forceinline__ bf16x8_t mx_ones(uint32_t bits) {
   uint32_t w[4];
@@ -213,7 +258,8 @@ __device__ __forceinline__ Words<N> load_words(const uint8_t* p) {
 // The packed rows of a workgroup: per sequence the (row, head of the group) pairs, group
 // fastest, in tiles of kRows. Sequence i's tiles are numbered from floor(start_i group /
 // kRows) + i: that leaves each at least as many numbers as it has tiles, without a scan of
-// the lengths; numbers without a tile have first >= count.
+// the lengths; numbers without a tile have first >= count. For a prefix a group of sequences
+// takes the place of a sequence, with the rows of all of them.
 struct MxRows {
   int seq;
   int64_t r0;     // the sequence's first row in the packed tensors
@@ -221,24 +267,67 @@ struct MxRows {
   int first;      // the tile's first packed row
   int kv_len;
   int back;       // position of the sequence's first row
+  int from;       // kMxOwn: the first token that is not its group's, a multiple of kMxShared
+  bool shared;    // kMxOwn: the prefix's pieces hold for it
 };
 
+template <MxPart PART>
+__device__ __forceinline__ int64_t mx_part_start(const MxAttnArgs& a, int i) {
+  if constexpr (PART == kMxPrefix) {
+    const int s = a.prefix.starts[i];
+    return mx_row_start(a.b, s < 0 ? 0 : (s < a.b.batch ? s : a.b.batch));
+  }
+  return mx_row_start(a.b, i);
+}
+
+__device__ __forceinline__ int mx_prefix_len(const MxAttnArgs& a, int group) {
+  const int64_t v = a.prefix.lens[group], most = (int64_t)a.prefix.max_pages << a.b.page_shift;
+  return (int)(v < 0 ? 0 : (v > most ? most : v)) & -kMxShared;
+}
+
+// what the rows of sequence (or group) i see, and of a sequence what its group has seen for it
+template <MxPart PART>
+__device__ __forceinline__ void mx_rows_see(const MxAttnArgs& a, int i, int64_t r1, MxRows& r) {
+  r.from = 0;
+  r.shared = false;
+  if constexpr (PART == kMxPrefix) {
+    r.kv_len = mx_prefix_len(a, i);
+    r.back = 0;
+    return;
+  }
+  r.kv_len = mx_seq_len(a.b, i);
+  r.back = r.kv_len - (int)(r1 - r.r0);
+  if constexpr (PART == kMxOwn) {
+    int lo = 0, hi = a.prefix.groups;  // the last group that starts at or before it
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.prefix.starts[mid] <= i) lo = mid;
+      else hi = mid;
+    }
+    if (a.prefix.starts[lo] <= i && i < a.prefix.starts[lo + 1]) {
+      const int len = mx_prefix_len(a, lo);
+      r.shared = len <= (a.causal ? r.back + 1 : r.kv_len);  // its first row sees all of it
+      r.from = r.shared ? len : 0;
+    }
+  }
+}
+
+template <MxPart PART = kMxWhole>
 __device__ __forceinline__ MxRows mx_rows(const MxAttnArgs& a, int64_t tile, int rows) {
-  int lo = 0, hi = a.b.batch;
+  int lo = 0, hi = PART == kMxPrefix ? a.prefix.groups : a.b.batch;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (mx_row_start(a.b, mid) * a.group / rows + mid <= tile) lo = mid;
+    if (mx_part_start<PART>(a, mid) * a.group / rows + mid <= tile) lo = mid;
     else hi = mid;
   }
   MxRows r;
-  const int64_t r1 = mx_row_start(a.b, lo + 1);
+  const int64_t r1 = mx_part_start<PART>(a, lo + 1);
   r.seq = lo;
-  r.r0 = mx_row_start(a.b, lo);
+  r.r0 = mx_part_start<PART>(a, lo);
   r.count = r1 > r.r0 ? (int)((r1 - r.r0) * a.group) : 0;
   const int64_t first = (tile - (r.r0 * a.group / rows + lo)) * rows;
   r.first = first < 0 || first > r.count ? r.count : (int)first;
-  r.kv_len = mx_seq_len(a.b, lo);
-  r.back = r.kv_len - (int)(r1 - r.r0);
+  mx_rows_see<PART>(a, lo, r1, r);
   return r;
 }
 
@@ -250,8 +339,7 @@ __device__ __forceinline__ MxRows mx_rows_of(const MxAttnArgs& a, int seq) {
   r.r0 = mx_row_start(a.b, seq);
   r.count = r1 > r.r0 ? (int)((r1 - r.r0) * a.group) : 0;
   r.first = 0;
-  r.kv_len = mx_seq_len(a.b, seq);
-  r.back = r.kv_len - (int)(r1 - r.r0);
+  mx_rows_see<kMxWhole>(a, seq, r1, r);
   return r;
 }
 
@@ -270,10 +358,32 @@ __device__ __forceinline__ int mx_low(const MxAttnArgs& a, int pos) {
   return a.window > 0 && pos - a.window + 1 > 0 ? pos - a.window + 1 : 0;
 }
 
+// (Rows that see a group's prefix see all of it; of what is left, masks by the last token only.)
+template <MxPart PART = kMxWhole>
 __device__ __forceinline__ MxSight mx_sight(const MxAttnArgs& a, const MxRows& r, int p0, int p1) {
+  if constexpr (PART == kMxPrefix) return MxSight{r.kv_len, r.kv_len, 0, 0, 0};
   const int pos_a = r.back + p0 / a.group, pos_b = r.back + (p1 - 1) / a.group;
+  if constexpr (PART == kMxOwn) return MxSight{mx_high(a, r.kv_len, pos_a), mx_high(a, r.kv_len, pos_b), r.from, r.from, 0};
   return MxSight{mx_high(a, r.kv_len, pos_a), mx_high(a, r.kv_len, pos_b), mx_low(a, pos_a), mx_low(a, pos_b),
                  a.window > 0 ? a.sinks : 0};
+}
+
+// the tokens [low, high) that packed row p sees (but for first tokens below sinks)
+template <MxPart PART>
+__device__ __forceinline__ int mx_row_high(const MxAttnArgs& a, const MxRows& r, int i) {
+  return PART == kMxPrefix ? r.kv_len : mx_high(a, r.kv_len, r.back + i);
+}
+
+template <MxPart PART>
+__device__ __forceinline__ int mx_row_low(const MxAttnArgs& a, const MxRows& r, int i) {
+  return PART == kMxWhole ? mx_low(a, r.back + i) : r.from;
+}
+
+// the block table's row of the sequence or group
+template <MxPart PART>
+__device__ __forceinline__ const int32_t* mx_table(const MxAttnArgs& a, const MxRows& r) {
+  return PART == kMxPrefix ? a.prefix.block_table + (int64_t)r.seq * a.prefix.table_stride
+                           : a.b.block_table + (int64_t)r.seq * a.b.table_stride;
 }
 
 // The tiles of `size` tokens that those rows see: the ones that hold first tokens, then

@@ -71,7 +71,7 @@ struct Lds {
 
 constexpr int waves_per_simd(int d) { return d == 64 ? 3 : d == 128 ? 2 : 1; }  // by registers
 
-template <int D>
+template <int D, MxPart PART>
 __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D)) void mx_attention_prompt_kernel(MxAttnArgs a) {
   using L = Lds<D>;
   constexpr int KS = D / 16, DB = D / 32;
@@ -84,10 +84,10 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D)) void mx_attention_p
   const int split = blockIdx.y;
   const int g = a.group;
   // within a causal sequence the last tiles see the most tokens: they are started first
-  const MxRows rows = mx_rows(a, (gridDim.x - 1 - blockIdx.x) / a.c.kv_heads, kRows);
-  if (rows.first >= rows.count || rows.count <= a.skip) return;  // the whole workgroup
+  const MxRows rows = mx_rows<PART>(a, (gridDim.x - 1 - blockIdx.x) / a.c.kv_heads, kRows);
+  if (rows.first >= rows.count || (PART == kMxWhole && rows.count <= a.skip)) return;  // the whole workgroup
   const int wg_end = rows.first + kRows < rows.count ? rows.first + kRows : rows.count;
-  const MxSight all = mx_sight(a, rows, rows.first, wg_end);
+  const MxSight all = mx_sight<PART>(a, rows, rows.first, wg_end);
   const MxSpan span = mx_span(all, kTile);
   const int begin = mx_share(span.count, split, a.splits), end = mx_share(span.count, split + 1, a.splits);
 
@@ -95,7 +95,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D)) void mx_attention_p
   const int p0 = rows.first + wave * 32;
   const int p1 = p0 + 32 < rows.count ? p0 + 32 : rows.count;
   MxSight sight{0, 0, 0, 0, 0};  // a wave without rows sees nothing
-  if (p0 < p1) sight = mx_sight(a, rows, p0, p1);
+  if (p0 < p1) sight = mx_sight<PART>(a, rows, p0, p1);
   if (p1 - p0 < 32) sight.high_min = 0;
   const int pn = p0 + n;
   const bool real = pn < rows.count;
@@ -109,8 +109,8 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D)) void mx_attention_p
       q[s] = as_bf16x8(w[0], w[1], w[2], w[3]);
     }
   }
-  const int high = real ? mx_high(a, rows.kv_len, rows.back + pn / g) : 0;
-  const int low = mx_low(a, rows.back + pn / g);
+  const int high = real ? mx_row_high<PART>(a, rows, pn / g) : 0;
+  const int low = mx_row_low<PART>(a, rows, pn / g);
 
   // ---- a tile's way into LDS: wave w brings tokens 16 w .. + 15 ----
   // K: four lanes to a token, D / 4 elements each; V: D / 16 elements of four tokens
@@ -131,7 +131,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D)) void mx_attention_p
     int64_t row;
     uint32_t there;
   };
-  const int32_t* table = a.b.block_table + (int64_t)rows.seq * a.b.table_stride;
+  const int32_t* table = mx_table<PART>(a, rows);
   const int pages = (rows.kv_len + (1 << a.b.page_shift) - 1) >> a.b.page_shift;
   int entry = 0, base = -64;
   bool holes = false;  // among the 64
@@ -447,7 +447,8 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D)) void mx_attention_p
   if (!real) return;
   const int64_t token = rows.r0 + pn / g;
   const int head = kvh * g + pn % g;
-  if (a.splits > 1) {
+  if (PART != kMxWhole || a.splits > 1) {
+    if (PART == kMxOwn && !rows.shared && split == 0 && h == 0) mx_drop_prefix(a, token, head);
     const int64_t at = ((int64_t)split * a.b.tokens + token) * a.heads + head;
     if (h == 0) a.part_ml[at] = make_float2(*ref, all_sum);
     if (all_sum != 0.0f) {
@@ -471,34 +472,51 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D)) void mx_attention_p
   }
 }
 
-template <int D>
+template <int D, MxPart PART>
 hipError_t launch_prompt(const MxAttnArgs& a, hipStream_t stream) {
-  const int64_t tiles = a.b.tokens * a.group / kRows + a.b.batch;
-  mx_attention_prompt_kernel<D>
+  const int64_t tiles = a.b.tokens * a.group / kRows + (PART == kMxPrefix ? a.prefix.groups : a.b.batch);
+  mx_attention_prompt_kernel<D, PART>
       <<<dim3((unsigned)(tiles * a.c.kv_heads), a.splits), 64 * kWaves, Lds<D>::Bytes, stream>>>(a);
   return hipGetLastError();
 }
 
-template <int D>
+template <int D, MxPart PART>
 hipError_t setup_prompt() {
-  return hipFuncSetAttribute((const void*)mx_attention_prompt_kernel<D>, hipFuncAttributeMaxDynamicSharedMemorySize,
+  return hipFuncSetAttribute((const void*)mx_attention_prompt_kernel<D, PART>, hipFuncAttributeMaxDynamicSharedMemorySize,
                              Lds<D>::Bytes);
+}
+
+template <MxPart PART>
+hipError_t setup_part() {
+  hipError_t e = setup_prompt<64, PART>();
+  if (e == hipSuccess) e = setup_prompt<128, PART>();
+  if (e == hipSuccess) e = setup_prompt<256, PART>();
+  return e;
+}
+
+template <MxPart PART>
+hipError_t launch_of(const MxAttnArgs& a, hipStream_t stream) {
+  switch (a.c.head_dim) {
+    case 64: return launch_prompt<64, PART>(a, stream);
+    case 128: return launch_prompt<128, PART>(a, stream);
+    default: return launch_prompt<256, PART>(a, stream);
+  }
 }
 
 }  // namespace
 
 hipError_t mx_attention_prompt_setup() {
-  hipError_t e = setup_prompt<64>();
-  if (e == hipSuccess) e = setup_prompt<128>();
-  if (e == hipSuccess) e = setup_prompt<256>();
+  hipError_t e = setup_part<kMxWhole>();
+  if (e == hipSuccess) e = setup_part<kMxPrefix>();
+  if (e == hipSuccess) e = setup_part<kMxOwn>();
   return e;
 }
 
-hipError_t launch_mx_attention_prompt(const MxAttnArgs& a, hipStream_t stream) {
-  switch (a.c.head_dim) {
-    case 64: return launch_prompt<64>(a, stream);
-    case 128: return launch_prompt<128>(a, stream);
-    default: return launch_prompt<256>(a, stream);
+hipError_t launch_mx_attention_prompt(const MxAttnArgs& a, MxPart part, hipStream_t stream) {
+  switch (part) {
+    case kMxWhole: return launch_of<kMxWhole>(a, stream);
+    case kMxPrefix: return launch_of<kMxPrefix>(a, stream);
+    default: return launch_of<kMxOwn>(a, stream);
   }
 }
 

@@ -1,0 +1,313 @@
+// mx_rope.hip - norms of query and key heads with their rotation, in one pass, and on into
+// the paged MXFP4 cache (gfx950).
+//
+//   n   = x w / sqrt(mean(x^2) + eps)                   of a head's D elements
+//   a'  = a cos t - b sin t,  b' = b cos t + a sin t     of the pairs (a, b) of n, t = position * freq
+//
+// bf16 in, one rounding to bf16 out; keys and values then become MXFP4 at their place in the
+// cache (mx_quant.hip does that alone).
+//
+// What bounds it is moving the bytes, each read and written once. A lane has 16 elements of
+// one head, so D / 16 lanes share a head and a step of a wave is 1024 / D heads of a token.
+// With pairs half the turned elements apart (j, j + R / 2) the 16 are the runs [8 l, + 8)
+// and [R / 2 + 8 l, + 8), otherwise one run: either way both elements of 8 pairs, no
+// exchange between lanes, and pair 8 l is the lane's first.
+//
+// A token's angles are the same for all of its heads: lane j finds cosine and sine of pair j
+// once, in fp64, and the wave keeps them in LDS. Queries are then fp32 throughout; keys
+// are fp64, because the step after their rounding to bf16 is one to 4 bits, where a last
+// bit that falls the other way can move the result by half of itself.
+#include <cmath>
+
+#include "mx_rope.hpp"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int kWaves = 4;
+
+// what one wave has in LDS
+template <int D>
+struct WaveLds {
+  double2 turn[D / 2];   // cosine, sine of each pair
+  float2 turnf[D / 2];
+  uint16_t k[1024];      // keys on their way into blocks of 32 consecutive elements
+};
+
+// orders a wave's own LDS writes before its reads by other lanes
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// cosine and sine of position * freq. The product is exact as hi + lo (31 and 24 bits), and
+// so is its first product with 1 / 2 pi as a sum; whole turns are dropped before they cost
+// bits: 2^-52 of a turn at every position.
+__device__ __forceinline__ double2 turn_of(int32_t position, float freq) {
+  constexpr double kInv = 0.15915494309189535, kInvLo = -9.839338337591243e-18;  // 1 / 2 pi
+  const double p = position, f = freq;
+  const double hi = p * f, lo = fma(p, f, -hi);
+  const double t = hi * kInv, e = fma(hi, kInv, -t) + fma(hi, kInvLo, lo * kInv);
+  const double r = (t - rint(t)) + e;
+  double s, c;
+  sincospi(2.0 * r, &s, &c);
+  return make_double2(c, s);
+}
+
+// RN_bf16 of a double: by way of fp32, whose rounding must not make or hide a tie
+__device__ __forceinline__ uint32_t bf16_of(double x) {
+  const float f = (float)x;
+  uint32_t b = __float_as_uint(f);
+  if ((b & 0xFFFFu) == 0x8000u) {
+    const double d = fabs(x) - (double)fabsf(f);
+    b += d > 0.0 ? 1u : d < 0.0 ? -1u : 0u;
+  }
+  if (f != f) return 0x7FC0u | b >> 31 << 15;
+  return (b + 0x7FFFu + (b >> 16 & 1u)) >> 16;
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  bf16x2_t c;
+  c[0] = (__bf16)lo;
+  c[1] = (__bf16)hi;
+  return as_u32(c);
+}
+
+struct Sixteen {
+  u32x4_t w[2];
+  __device__ __forceinline__ float at(int i) const {  // bf16 element i
+    const uint32_t x = w[i >> 3][(i >> 1) & 3];
+    return __uint_as_float(i & 1 ? x & 0xFFFF0000u : x << 16);
+  }
+};
+
+// the sum over the D / 16 lanes of a head
+template <int D, typename T>
+__device__ __forceinline__ T head_sum(T x) {
+#pragma unroll
+  for (int off = 1; off < D / 16; off <<= 1) x += __shfl_xor(x, off, 64);
+  return x;
+}
+
+// The last sequence that starts at or before the row, 64 candidates at a time (a binary
+// search is a load's latency for each factor of two).
+__device__ __forceinline__ int sequence_of(const MxBatch& b, int64_t row, int lane) {
+  int lo = 0, n = b.batch;
+  while (n > 1) {
+    const int step = (n + 63) >> 6, i = lane * step;
+    const bool at = i < n && b.cu_seqlens[lo + i] <= row;
+    const int below = __popcll(__ballot(at));
+    const int skip = below > 0 ? (below - 1) * step : 0;
+    lo += skip;
+    n = n - skip < step ? n - skip : step;
+  }
+  return lo;
+}
+
+// 16 consecutive elements a lane into the cache
+template <int D>
+__device__ __forceinline__ void put(const Sixteen& x, uint8_t* codes, uint8_t* scales, int64_t row, int sub, bool there) {
+  const u16x2_t m = mx_max2(mx_max2(mx_max2(mx_abs2(x.w[0][0]), mx_abs2(x.w[0][1])), mx_max2(mx_abs2(x.w[0][2]), mx_abs2(x.w[0][3]))),
+                            mx_max2(mx_max2(mx_abs2(x.w[1][0]), mx_abs2(x.w[1][1])), mx_max2(mx_abs2(x.w[1][2]), mx_abs2(x.w[1][3]))));
+  uint32_t top = m[0] > m[1] ? m[0] : m[1];
+  const uint32_t other = (uint32_t)__builtin_amdgcn_mov_dpp((int)top, 0xB1, 0xF, 0xF, false);  // lane ^ 1
+  top = top > other ? top : other;
+  const uint32_t byte = mx_scale_byte(top);
+  uint32_t all = byte << (8 * (sub >> 1 & 3));  // of the lanes of four blocks (of 64: two)
+  all |= (uint32_t)__builtin_amdgcn_mov_dpp((int)all, 0x4E, 0xF, 0xF, false);  // lane ^ 2
+  if (D > 64) all |= (uint32_t)__shfl_xor((int)all, 4, 64);
+  if (!there) return;
+  *(u32x2_t*)(codes + row * (D / 2) + sub * 8) = u32x2_t{mx_encode8(x.w[0], byte), mx_encode8(x.w[1], byte)};
+  if (D == 64) {
+    if (sub == 0) *(uint16_t*)(scales + row * (D / 32)) = (uint16_t)all;
+  } else {
+    if ((sub & 7) == 0) *(uint32_t*)(scales + row * (D / 32) + (sub >> 3) * 4) = all;
+  }
+}
+
+template <int D, bool APPEND, bool INTERLEAVED>
+__global__ __launch_bounds__(64 * kWaves) void mx_rope_kernel(MxRopeArgs a) {
+  constexpr int L = D / 16, H = 64 / L;  // lanes of a head, heads of a step
+  __shared__ __align__(16) WaveLds<D> lds[kWaves];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  WaveLds<D>& my = lds[wave];
+  const int64_t item = (int64_t)blockIdx.x * kWaves + wave;
+  const int64_t token = a.parts == 1 ? item : item / a.parts;
+  const int part = a.parts == 1 ? 0 : (int)(item - token * a.parts);
+  if (token >= a.tokens) return;
+  const int sub = lane % L, hl = lane / L;
+  const bool turns = sub < a.rotary / 16;
+  const int first = INTERLEAVED || !turns ? 16 * sub : 8 * sub;
+  const int second = INTERLEAVED || !turns ? first + 8 : a.rotary / 2 + 8 * sub;
+  const int qs = (a.heads + H - 1) / H, ks = APPEND ? (a.kv_heads + H - 1) / H : 0, steps = qs + 2 * ks;
+
+  auto load = [&](const uint16_t* head, int at0, int at1) __attribute__((always_inline)) {
+    Sixteen x;
+    x.w[0] = *(const u32x4_t*)(head + at0);
+    x.w[1] = *(const u32x4_t*)(head + at1);
+    return x;
+  };
+  // what step s of the token reads; lanes without a head read the last one's
+  auto fetch = [&](int s) __attribute__((always_inline)) {
+    if (!APPEND || s < qs) {
+      const int head = s * H + hl < a.heads ? s * H + hl : a.heads - 1;
+      return load(a.q + token * a.q_token + head * a.q_head, first, second);
+    }
+    const bool is_v = s >= qs + ks;
+    const int h = (s - (is_v ? qs + ks : qs)) * H + hl, head = h < a.kv_heads ? h : a.kv_heads - 1;
+    return is_v ? load(a.v + token * a.v_token + head * a.v_head, 16 * sub, 16 * sub + 8)
+                : load(a.k + token * a.k_token + head * a.k_head, first, second);
+  };
+  Sixteen next = fetch(part);
+
+  // ---- where the token belongs ----
+  int pos = 0;
+  int64_t page = -1;
+  if (APPEND) {
+    const int seq = sequence_of(a.b, token, lane);
+    const int64_t r0 = mx_row_start(a.b, seq), r1 = mx_row_start(a.b, seq + 1);
+    if (token < r0 || token >= r1) return;  // of no sequence
+    pos = mx_seq_len(a.b, seq) - (int)(r1 - token);
+    if (pos >= 0) {
+      const int64_t p = a.b.block_table[(int64_t)seq * a.b.table_stride + (pos >> a.b.page_shift)];
+      if (p >= 0 && p < a.b.num_pages) page = p;
+    }
+  }
+
+  // ---- the angles ----
+  if (part < qs + ks) {
+    for (int j = lane; j < a.rotary / 2; j += 64) {
+      int at = pos;
+      if (a.positions) {
+        int axis = a.axes ? a.axes[j] : 0;
+        axis = axis < 0 ? 0 : axis < a.axis_count ? axis : a.axis_count - 1;
+        at = a.positions[token * a.pos_token + axis * a.pos_axis];
+      }
+      const double2 t = turn_of(at, a.freqs[j]);
+      my.turn[j] = t;
+      my.turnf[j] = make_float2((float)t.x, (float)t.y);
+    }
+    wave_sync();
+  }
+
+  for (int s = part; s < steps; s += a.parts) {
+    const Sixteen x = next;
+    if (s + a.parts < steps) next = fetch(s + a.parts);
+    if (!APPEND || s < qs) {
+      // ---- queries: fp32 ----
+      const int head = s * H + hl;
+      float y[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) y[i] = x.at(i);
+      if (a.q_norm.on) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum = fmaf(y[i], y[i], sum);
+        sum = head_sum<D>(sum);
+        Sixteen w;
+        if (a.q_norm.weight) w = load(a.q_norm.weight, first, second);
+        else w.w[0] = w.w[1] = u32x4_t{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+        if (__any(!(sum > 0x1p-80f && sum < 0x1p100f))) {  // squares may have left fp32's range
+          double d = 0.0;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) d = fma((double)y[i], (double)y[i], d);
+          const double r = 1.0 / sqrt(head_sum<D>(d) / D + a.q_norm.eps);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) y[i] = (float)((double)y[i] * r * (double)w.at(i));
+        } else {
+          const float r = 1.0f / sqrtf(sum * (1.0f / D) + (float)a.q_norm.eps);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) y[i] = y[i] * r * w.at(i);
+        }
+      }
+      if (turns) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float2 t = my.turnf[8 * sub + j];
+          float &p = y[INTERLEAVED ? 2 * j : j], &q = y[INTERLEAVED ? 2 * j + 1 : j + 8];
+          const float u = p, v = q;
+          p = fmaf(u, t.x, -(v * t.y));
+          q = fmaf(v, t.x, u * t.y);
+        }
+      }
+      if (head < a.heads) {
+        uint16_t* dst = a.out + token * a.out_token + head * a.out_head;
+        *(u32x4_t*)(dst + first) = u32x4_t{pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7])};
+        *(u32x4_t*)(dst + second) = u32x4_t{pack2(y[8], y[9]), pack2(y[10], y[11]), pack2(y[12], y[13]), pack2(y[14], y[15])};
+      }
+      continue;
+    }
+    // ---- keys and values ----
+    const bool is_v = s >= qs + ks;
+    const int head = (s - (is_v ? qs + ks : qs)) * H + hl;
+    Sixteen z = x;
+    if (!is_v) {
+      double y[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) y[i] = x.at(i);
+      if (a.k_norm.on) {
+        double sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum = fma(y[i], y[i], sum);
+        const double r = 1.0 / sqrt(head_sum<D>(sum) / D + a.k_norm.eps);
+        Sixteen w;
+        if (a.k_norm.weight) w = load(a.k_norm.weight, first, second);
+        else w.w[0] = w.w[1] = u32x4_t{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i] = y[i] * r * (double)w.at(i);
+      }
+      if (turns) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const double2 t = my.turn[8 * sub + j];
+          double &p = y[INTERLEAVED ? 2 * j : j], &q = y[INTERLEAVED ? 2 * j + 1 : j + 8];
+          const double u = p, v = q;
+          p = fma(u, t.x, -(v * t.y));
+          q = fma(v, t.x, u * t.y);
+        }
+      }
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = bf16_of(y[2 * i]) | bf16_of(y[2 * i + 1]) << 16;
+      z.w[0] = u32x4_t{w[0], w[1], w[2], w[3]};
+      z.w[1] = u32x4_t{w[4], w[5], w[6], w[7]};
+      if (!INTERLEAVED && a.rotary > 0) {
+        *(u32x4_t*)(my.k + hl * D + first) = z.w[0];
+        *(u32x4_t*)(my.k + hl * D + second) = z.w[1];
+        wave_sync();
+        z = load(my.k + hl * D, 16 * sub, 16 * sub + 8);
+        wave_sync();
+      }
+    }
+    const int64_t row = (((page < 0 ? 0 : page) * a.c.kv_heads + head) << a.b.page_shift) + (pos & ((1 << a.b.page_shift) - 1));
+    put<D>(z, is_v ? a.c.v_codes : a.c.k_codes, is_v ? a.c.v_scales : a.c.k_scales, row, sub, page >= 0 && head < a.kv_heads);
+  }
+}
+
+template <int D>
+void launch_dim(const MxRopeArgs& a, bool append, bool interleaved, hipStream_t stream) {
+  const unsigned groups = (unsigned)((a.tokens * a.parts + kWaves - 1) / kWaves);
+  if (append) {
+    if (interleaved) mx_rope_kernel<D, true, true><<<groups, 64 * kWaves, 0, stream>>>(a);
+    else mx_rope_kernel<D, true, false><<<groups, 64 * kWaves, 0, stream>>>(a);
+  } else {
+    if (interleaved) mx_rope_kernel<D, false, true><<<groups, 64 * kWaves, 0, stream>>>(a);
+    else mx_rope_kernel<D, false, false><<<groups, 64 * kWaves, 0, stream>>>(a);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_mx_rope(const MxRopeArgs& a, int head_dim, bool append, bool interleaved, hipStream_t stream) {
+  switch (head_dim) {
+    case 64: launch_dim<64>(a, append, interleaved, stream); break;
+    case 128: launch_dim<128>(a, append, interleaved, stream); break;
+    default: launch_dim<256>(a, append, interleaved, stream); break;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace nvfp4

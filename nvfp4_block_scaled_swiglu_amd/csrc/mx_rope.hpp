@@ -1,0 +1,47 @@
+// mx_rope.hpp - arguments of the head norm and rotation kernels.
+#pragma once
+
+#include "mx.hpp"
+
+namespace nvfp4 {
+
+struct MxNorm {
+  const uint16_t* weight;  // bf16 [head_dim], or null: ones
+  double eps;
+  bool on;
+};
+
+struct MxRopeArgs {
+  MxBatch b;  // append only, as the cache
+  MxCache c;
+  // rotation
+  const float* freqs;        // [rotary / 2]
+  const int32_t* axes;       // [rotary / 2], or null: axis 0
+  const int32_t* positions;  // or null: the row's position in its sequence
+  int64_t pos_token, pos_axis;
+  int axis_count, rotary;    // rotary 0: none
+  MxNorm q_norm, k_norm;
+  const uint16_t* q;
+  uint16_t* out;
+  const uint16_t* k;
+  const uint16_t* v;
+  int64_t q_token, q_head, out_token, out_head, k_token, k_head, v_token, v_head;  // element strides
+  int64_t tokens;
+  int heads, kv_heads;       // kv_heads 0: no cache
+  int parts;                 // waves of a token
+};
+
+// Waves of a token: one, which finds the angles once for all heads, where the tokens alone
+// are two waves for every SIMD; otherwise up to one for each step of the token's work
+// (64 / (head_dim / 16) heads of q, k or v).
+inline int64_t mx_rope_parts(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim) {
+  const int64_t per = 1024 / head_dim;
+  const int64_t steps = (heads + per - 1) / per + 2 * ((kv_heads + per - 1) / per);
+  int64_t parts = tokens > 0 ? (2048 + tokens - 1) / tokens : 1;
+  if (parts > steps) parts = steps;
+  return parts < 1 ? 1 : parts;
+}
+
+hipError_t launch_mx_rope(const MxRopeArgs& a, int head_dim, bool append, bool interleaved, hipStream_t stream);
+
+}  // namespace nvfp4

@@ -8,6 +8,10 @@ matrix instructions multiply as it is stored. Functions carry the C names:
 * ``mxfp4_gemm_bf16out(a, w)``                               - product of two, BF16 out, from one row up
 * ``mxfp4_cache_append(...)``, ``mxfp4_cache_read(...)``     - a paged key/value cache in MXFP4
 * ``mxfp4_attention(q, cache, ...)``                         - attention over that cache
+* ``mxfp4_attention_prefix(q, cache, ...)``                  - where groups of sequences share their first pages
+* ``mxfp4_norm_rope(x, ...)``, ``mxfp4_norm_rope_append(...)`` - head norms and rotation, and on into the cache
+  (``mxfp4_rope.py``)
+* ``mxfp4_pages_*(...)``, ``mxfp4_cache_copy(...)``           - which pages the sequences hold (``mxfp4_pages.py``)
 
 As elsewhere in the package every step runs in the library's kernels, a failing call raises
 (strict) or returns None and counts a fallback, and outputs that the caller does not pass are
@@ -46,8 +50,31 @@ class _CBatch(ctypes.Structure):
                 ("table_stride", _I64), ("tokens", _I64)]
 
 
+class _CPrefix(ctypes.Structure):
+    _fields_ = [("block_table", _P), ("lens", _P), ("group_starts", _P), ("groups", _I64), ("max_pages", _I64),
+                ("table_stride", _I64)]
+
+
+class _CNorm(ctypes.Structure):
+    _fields_ = [("weight", _P), ("eps", ctypes.c_double)]
+
+
+class _CRotation(ctypes.Structure):
+    _fields_ = [("freqs", _P), ("axes_dev", _P), ("positions", _P), ("rotary_dim", _I64), ("axes", _I64),
+                ("token_stride", _I64), ("axis_stride", _I64), ("interleaved", _INT)]
+
+
+class _CPages(ctypes.Structure):
+    _fields_ = [("block_table", _P), ("seq_lens", _P), ("refs", _P), ("slots", _I64), ("max_pages", _I64),
+                ("table_stride", _I64), ("num_pages", _I64), ("page_size", _I64)]
+
+
 _PC = ctypes.POINTER(_CCache)
 _PB = ctypes.POINTER(_CBatch)
+_PX = ctypes.POINTER(_CPrefix)
+_PN = ctypes.POINTER(_CNorm)
+_PR = ctypes.POINTER(_CRotation)
+_PP = ctypes.POINTER(_CPages)
 
 # Every symbol include/mxfp4.h declares, with (restype, argtypes).
 SIGNATURES = {
@@ -63,6 +90,19 @@ SIGNATURES = {
     "mxfp4_attention_workspace_bytes": (_I64, [_PC, _PB, _I64, _I64, _I64, _I64]),
     "mxfp4_attention": (_INT, [_PC, _PB, _P, _I64, _I64, _I64, ctypes.c_float, _INT, _I64, _I64, _I64, _P, _I64, _I64,
                                _P, _I64, _P]),
+    "mxfp4_attention_prefix_workspace_bytes": (_I64, [_PC, _PB, _PX, _I64, _I64, _I64]),
+    "mxfp4_attention_prefix": (_INT, [_PC, _PB, _PX, _P, _I64, _I64, _I64, ctypes.c_float, _INT, _I64, _I64, _P, _I64,
+                                      _I64, _P, _I64, _P]),
+    "mxfp4_norm_rope": (_INT, [_P, _I64, _I64, _I64, _I64, _I64, _PN, _PR, _P, _I64, _I64, _P]),
+    "mxfp4_norm_rope_append": (_INT, [_PC, _PB, _P, _I64, _I64, _I64, _PN, _P, _I64, _I64, _PN, _P, _I64, _I64, _PR, _P,
+                                      _I64, _I64, _P]),
+    "mxfp4_pages_free": (_INT, [_PP, _P, _P, _I64, _P]),
+    "mxfp4_pages_fork": (_INT, [_PP, _P, _P, _I64, _P, _P]),
+    "mxfp4_pages_reserve_workspace_bytes": (_I64, [_PP, _I64]),
+    "mxfp4_pages_reserve": (_INT, [_PP, _P, _P, _I64, _P, _P, _P, _P, _I64, _P]),
+    "mxfp4_pages_compact_workspace_bytes": (_I64, [_PP]),
+    "mxfp4_pages_compact": (_INT, [_PP, _P, _I64, _P, _P, _P, _P, _P, _I64, _P]),
+    "mxfp4_cache_copy": (_INT, [_PC, _PC, _P, _P, _I64, _P]),
 }
 
 
@@ -457,6 +497,90 @@ def mxfp4_attention_workspace_bytes(cache: Mxfp4Cache, block_table, seq_lens, cu
     c, _ = _cache(cache)
     b, _ = _batch(block_table, seq_lens, cu_seqlens, tokens)
     size = int(nv.lib().mxfp4_attention_workspace_bytes(c, b, heads, max_kv, window, sinks))
+    if size < 0:
+        raise ValueError(nv.lib().nvfp4_last_error().decode(errors="replace"))
+    return size
+
+
+# ---- attention behind shared prefixes ------------------------------------------------------
+
+def _prefix(prefix_table, prefix_lens, group_starts):
+    _int32(prefix_table, "prefix_table", 2)
+    _int32(prefix_lens, "prefix_lens", 1)
+    _int32(group_starts, "group_starts", 1)
+    groups, pages = prefix_table.shape
+    if prefix_lens.shape[0] != groups or group_starts.shape[0] != groups + 1:
+        raise ValueError("prefix_table, prefix_lens and group_starts disagree about the groups")
+    stride = prefix_table.stride(0) if groups > 1 else pages
+    return (_CPrefix(prefix_table.data_ptr(), prefix_lens.data_ptr(), group_starts.data_ptr(), groups, pages, stride),
+            (prefix_table, prefix_lens, group_starts))
+
+
+def _most(given: Optional[int], pages: int, page_size: int) -> int:
+    most = max(1, pages * page_size) if given is None else given
+    if not -_MOST <= most <= _MOST:
+        raise ValueError("max_prefix and max_own must fit 64 bits")
+    return most
+
+
+def mxfp4_attention_prefix(q, cache: Mxfp4Cache, block_table, seq_lens, cu_seqlens, prefix_table, prefix_lens, group_starts,
+                           scale: Optional[float] = None, causal: bool = True, max_prefix: Optional[int] = None,
+                           max_own: Optional[int] = None, out=None, workspace=None, stream=None,
+                           strict: Optional[bool] = None):
+    """mxfp4_attention (without a window) of sequences whose groups share their first tokens, which
+    are then read once for a group.
+
+    Group g is the sequences group_starts[g] .. group_starts[g + 1] - 1 (int32 [groups + 1],
+    ascending); the first prefix_lens[g] // 64 * 64 of their tokens are those in the pages of
+    prefix_table[g] (int32 [groups, max_pages]). Other tokens go by block_table, and so do all tokens of
+    sequences in no group or whose first row does not see every shared token. max_prefix, max_own: the
+    longest prefix, and the most tokens of a sequence behind its own, as far as known (by default
+    what the tables could hold); they decide how the work is split. workspace: a uint8 tensor of at least
+    mxfp4_attention_prefix_workspace_bytes(...) bytes, allocated by default."""
+    import torch
+    c, ct = _cache(cache)
+    _bf16(q, "q", 3)
+    tokens, heads, dim = q.shape
+    if dim != c.head_dim:
+        raise ValueError(f"q has head_dim {dim}, the cache {c.head_dim}")
+    b, bt = _batch(block_table, seq_lens, cu_seqlens, tokens)
+    x, xt = _prefix(prefix_table, prefix_lens, group_starts)
+    if scale is None:
+        scale = dim ** -0.5
+    max_prefix, max_own = _most(max_prefix, x.max_pages, c.page_size), _most(max_own, b.max_pages, c.page_size)
+    with _On(stream, q, *ct, *bt, *xt) as on:
+        if out is None:
+            out = torch.empty((tokens, heads, dim), dtype=torch.bfloat16, device=on.device)
+        elif _bf16(out, "out", 3, q.shape).device != on.device:
+            raise ValueError("out must be on the device of q")
+        else:
+            on.use(out)
+        if workspace is None:
+            size = nv.lib().mxfp4_attention_prefix_workspace_bytes(c, b, x, heads, max_prefix, max_own)
+            if size > 0:
+                workspace = torch.empty((size,), dtype=torch.uint8, device=on.device)
+        elif _buffer(workspace, "workspace", 0).device != on.device:
+            raise ValueError("workspace must be on the device of q")
+        else:
+            on.use(workspace)
+        if not nv._call("mxfp4_attention_prefix", c, b, x, q.data_ptr(), *_strides(q), heads, scale, int(bool(causal)),
+                        max_prefix, max_own, out.data_ptr(), *_strides(out), 0 if workspace is None else workspace.data_ptr(),
+                        0 if workspace is None else workspace.numel(), on.handle, strict=strict):
+            return None
+    return out
+
+
+def mxfp4_attention_prefix_workspace_bytes(cache: Mxfp4Cache, block_table, seq_lens, cu_seqlens, prefix_table, prefix_lens,
+                                           group_starts, tokens: int, heads: int, max_prefix: Optional[int] = None,
+                                           max_own: Optional[int] = None) -> int:
+    """Bytes of the workspace of a call of these sizes; raises ValueError where the call would be refused."""
+    if not (-_MOST <= tokens <= _MOST and -_MOST <= heads <= _MOST):
+        raise ValueError("tokens and heads must fit 64 bits")
+    c, _ = _cache(cache)
+    b, _ = _batch(block_table, seq_lens, cu_seqlens, tokens)
+    x, _ = _prefix(prefix_table, prefix_lens, group_starts)
+    size = int(nv.lib().mxfp4_attention_prefix_workspace_bytes(
+        c, b, x, heads, _most(max_prefix, x.max_pages, c.page_size), _most(max_own, b.max_pages, c.page_size)))
     if size < 0:
         raise ValueError(nv.lib().nvfp4_last_error().decode(errors="replace"))
     return size
