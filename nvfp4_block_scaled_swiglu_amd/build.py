@@ -29,7 +29,8 @@ FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=o
 # the other forms come out the same either way, those of 64 and 128 with 9 and 8 spilled.
 EXTRA_FLAGS = {"producer.hip": ["-mllvm", "-amdgpu-atomic-optimizer-strategy=None"],
                "mx_attn.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
-               "mx_attn_prompt.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+               "mx_attn_prompt.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+               "mx_attn_prefix.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 
 
 def _compile(src: str, verbose: bool) -> str:

@@ -118,6 +118,23 @@ __device__ __forceinline__ int mx_seq_len(const MxBatch& b, int i) {
   return (int)(v < 0 ? 0 : (v > most ? most : v));
 }
 
+// The last i of [0, n) for which at(i), which holds up to some i and not beyond (0 if nowhere): 64
+// candidates at a time, one a lane, because every step waits for a load. All lanes take part.
+template <typename F>
+__device__ __forceinline__ int mx_last(int n, F at) {
+  const int lane = __lane_id();
+  int lo = 0;
+  while (n > 1) {
+    const int step = (n + 63) >> 6, i = lane * step;
+    const bool yes = i < n && at(lo + i);
+    const int below = __popcll(__ballot(yes));
+    const int skip = below > 0 ? (below - 1) * step : 0;
+    lo += skip;
+    n = n - skip < step ? n - skip : step;
+  }
+  return __builtin_amdgcn_readfirstlane(lo);
+}
+
 // Where packed row `row` lives in the cache: its sequence is the last one that starts at
 // or before it. False for a row of no sequence; otherwise pos is its position (negative
 // if the sequence is shorter than its rows) and page its page, or -1 if that is not there.

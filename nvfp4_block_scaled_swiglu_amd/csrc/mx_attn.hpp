@@ -18,8 +18,8 @@ struct MxPrefix {
 constexpr int kMxShared = 64;  // tokens: whole tiles of either form
 
 // Which tokens a launch is for: all that its rows see, a group's prefix for the rows of all of
-// its sequences, or what is left of each sequence.
-enum MxPart { kMxWhole, kMxPrefix, kMxOwn };
+// its sequences, what is left of each sequence, or all again, the prefix by its group's table.
+enum MxPart { kMxWhole, kMxPrefix, kMxOwn, kMxThrough };
 
 struct MxAttnArgs {
   MxBatch b;
@@ -35,9 +35,10 @@ struct MxAttnArgs {
   float2* part_ml;  // [splits, tokens, heads] reference score and sum; by_seq likewise
   int skip;         // prompt form: sequences of up to so many packed rows are not its own
   bool by_seq;      // few-rows form: a workgroup a sequence and kv head, of up to 16 packed rows
+  int tiles;        // kMxPrefix and kMxOwn: row tiles of the launch
   MxPrefix prefix;  // kMxPrefix and kMxOwn, whose launches always leave pieces
-  float2* prefix_ml;      // kMxOwn: the prefix's pieces, [prefix_splits, tokens, heads]
-  int prefix_splits;
+  int prefix_splits;        // joins: the first pieces are a prefix's, 0: none
+  uint32_t* shared;         // [tokens] whether they hold for the row, written by kMxOwn for the join
 };
 
 constexpr int kMxMostSplits = 256;  // that a join takes
@@ -129,25 +130,41 @@ inline int64_t mx_part_bytes(const MxAttnPlan& p, int64_t tokens, int64_t batch,
 // A call with shared prefixes: what the groups' rows see of them, and the rest of the sequences.
 struct MxPrefixPlan {
   MxAttnPlan prefix, own;
+  bool through;  // no parts: each sequence's rows over all of their tokens, by own (prompt form)
 };
+
+constexpr int kMxJoinTokens = 800;
 
 inline MxPrefixPlan mx_prefix_plan(int64_t tokens, int64_t batch, int64_t groups, int64_t heads, int64_t kv_heads,
                                    int64_t head_dim, int64_t max_prefix, int64_t max_own) {
   MxPrefixPlan p;
-  p.prefix = mx_attention_plan(tokens, groups < tokens ? groups : tokens, heads, kv_heads, head_dim, max_prefix, 0, 0);
   p.own = mx_attention_plan(tokens, batch, heads, kv_heads, head_dim, max_own, 0, 0);
+  p.prefix = mx_attention_plan(tokens, groups < tokens ? groups : tokens, heads, kv_heads, head_dim, max_prefix, 0, 0);
+  const int64_t rows = tokens * (heads / kv_heads);
+  const int64_t own_tiles = batch > 0 ? ((rows + batch - 1) / batch + 127) / 128 * batch : 0;
+  const int64_t prefix_tiles = ((rows + groups - 1) / groups + 127) / 128 * groups;
+  p.through = !p.own.few && (own_tiles - prefix_tiles) * max_prefix <= kMxJoinTokens * own_tiles;
+  if (p.through) p.own = mx_attention_plan(tokens, batch, heads, kv_heads, head_dim, max_prefix + max_own, 0, 0);
   p.prefix.mixed = p.own.mixed = 0;
   if (p.prefix.splits > kMxMostSplits / 2) p.prefix.splits = kMxMostSplits / 2;
   if (p.own.splits > kMxMostSplits / 2) p.own.splits = kMxMostSplits / 2;
   return p;
 }
 
+// row tiles of a launch, by their numbering (mx_rows)
+inline int64_t mx_part_tiles(int64_t packed, int64_t sequences, int rows) {
+  return (packed + rows - 1) / rows + sequences - 1;
+}
+
 inline int64_t mx_prefix_bytes(const MxPrefixPlan& p, int64_t tokens, int64_t heads, int64_t head_dim) {
-  return ((p.prefix.splits + p.own.splits) * tokens * heads * (head_dim + 2) * 4 + 15) / 16 * 16;
+  if (p.through) return mx_prompt_part_bytes(p.own, tokens, heads, head_dim);
+  return ((p.prefix.splits + p.own.splits) * tokens * heads * (head_dim + 2) * 4 + tokens * 4 + 15) / 16 * 16;
 }
 
 hipError_t mx_attention_prompt_setup();
-hipError_t launch_mx_attention_prompt(const MxAttnArgs& a, MxPart part, hipStream_t stream);
+hipError_t launch_mx_attention_prompt(const MxAttnArgs& a, hipStream_t stream);
+hipError_t mx_attention_prefix_setup();
+hipError_t launch_mx_attention_join_parts(const MxAttnArgs& a, hipStream_t stream);
 
 // ---- device side ----
 
@@ -215,12 +232,6 @@ __device__ __forceinline__ uint32_t decode2(uint32_t q, float s, int sel) {
   }
 }
 
-// a row that reads all of its tokens itself: the prefix's pieces of its group are not its own
-__device__ __forceinline__ void mx_drop_prefix(const MxAttnArgs& a, int64_t token, int head) {
-  for (int s = 0; s < a.prefix_splits; ++s)
-    a.prefix_ml[((int64_t)s * a.b.tokens + token) * a.heads + head] = make_float2(-INFINITY, 0.0f);
-}
-
 // bits -> eight bf16 that are 1 where the bit is set
 __device__ __forceinline__ bf16x8_t mx_ones(uint32_t bits) {
   uint32_t w[4];
@@ -267,8 +278,9 @@ struct MxRows {
   int first;      // the tile's first packed row
   int kv_len;
   int back;       // position of the sequence's first row
-  int from;       // kMxOwn: the first token that is not its group's, a multiple of kMxShared
+  int from;       // kMxOwn, kMxThrough: the first token that is not its group's, a multiple of kMxShared
   bool shared;    // kMxOwn: the prefix's pieces hold for it
+  int prefix;     // kMxThrough: its group
 };
 
 template <MxPart PART>
@@ -288,7 +300,7 @@ __device__ __forceinline__ int mx_prefix_len(const MxAttnArgs& a, int group) {
 // what the rows of sequence (or group) i see, and of a sequence what its group has seen for it
 template <MxPart PART>
 __device__ __forceinline__ void mx_rows_see(const MxAttnArgs& a, int i, int64_t r1, MxRows& r) {
-  r.from = 0;
+  r.from = r.prefix = 0;
   r.shared = false;
   if constexpr (PART == kMxPrefix) {
     r.kv_len = mx_prefix_len(a, i);
@@ -297,29 +309,21 @@ __device__ __forceinline__ void mx_rows_see(const MxAttnArgs& a, int i, int64_t 
   }
   r.kv_len = mx_seq_len(a.b, i);
   r.back = r.kv_len - (int)(r1 - r.r0);
-  if constexpr (PART == kMxOwn) {
-    int lo = 0, hi = a.prefix.groups;  // the last group that starts at or before it
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.prefix.starts[mid] <= i) lo = mid;
-      else hi = mid;
-    }
+  if constexpr (PART == kMxOwn || PART == kMxThrough) {
+    const int lo = mx_last(a.prefix.groups, [&](int g) { return a.prefix.starts[g] <= i; });
     if (a.prefix.starts[lo] <= i && i < a.prefix.starts[lo + 1]) {
       const int len = mx_prefix_len(a, lo);
       r.shared = len <= (a.causal ? r.back + 1 : r.kv_len);  // its first row sees all of it
       r.from = r.shared ? len : 0;
+      r.prefix = lo;
     }
   }
 }
 
 template <MxPart PART = kMxWhole>
 __device__ __forceinline__ MxRows mx_rows(const MxAttnArgs& a, int64_t tile, int rows) {
-  int lo = 0, hi = PART == kMxPrefix ? a.prefix.groups : a.b.batch;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (mx_part_start<PART>(a, mid) * a.group / rows + mid <= tile) lo = mid;
-    else hi = mid;
-  }
+  const int lo = mx_last(PART == kMxPrefix ? a.prefix.groups : a.b.batch,
+                         [&](int i) { return mx_part_start<PART>(a, i) * a.group / rows + i <= tile; });
   MxRows r;
   const int64_t r1 = mx_part_start<PART>(a, lo + 1);
   r.seq = lo;
@@ -364,8 +368,34 @@ __device__ __forceinline__ MxSight mx_sight(const MxAttnArgs& a, const MxRows& r
   if constexpr (PART == kMxPrefix) return MxSight{r.kv_len, r.kv_len, 0, 0, 0};
   const int pos_a = r.back + p0 / a.group, pos_b = r.back + (p1 - 1) / a.group;
   if constexpr (PART == kMxOwn) return MxSight{mx_high(a, r.kv_len, pos_a), mx_high(a, r.kv_len, pos_b), r.from, r.from, 0};
+  if constexpr (PART == kMxThrough) return MxSight{mx_high(a, r.kv_len, pos_a), mx_high(a, r.kv_len, pos_b), 0, 0, 0};
   return MxSight{mx_high(a, r.kv_len, pos_a), mx_high(a, r.kv_len, pos_b), mx_low(a, pos_a), mx_low(a, pos_b),
                  a.window > 0 ? a.sinks : 0};
+}
+
+// Which piece, kv head and row tile a workgroup of a launch for a part has. Row tiles of a group read the
+// same tokens, so where pieces and kv heads divide over the 8 XCDs (workgroup i is on XCD i % 8)
+// those of one piece and kv head follow one another on one XCD, whose L2 then has them.
+struct MxPlace {
+  int split, kvh, tile;
+};
+
+__device__ __forceinline__ MxPlace mx_place(const MxAttnArgs& a, int id) {
+  const int kv = a.c.kv_heads, units = a.splits * kv;
+  int unit, tile;
+  if (units % 8 == 0) {
+    const int i = id >> 3;
+    tile = i % a.tiles;
+    unit = i / a.tiles * 8 + (id & 7);
+  } else {
+    unit = id % units;
+    tile = id / units;
+  }
+  return MxPlace{unit / kv, unit % kv, tile};
+}
+
+__device__ __forceinline__ MxPlace mx_place_whole(const MxAttnArgs& a) {
+  return MxPlace{(int)blockIdx.y, (int)blockIdx.x % a.c.kv_heads, (int)(gridDim.x - 1 - blockIdx.x) / a.c.kv_heads};
 }
 
 // the tokens [low, high) that packed row p sees (but for first tokens below sinks)
@@ -376,7 +406,7 @@ __device__ __forceinline__ int mx_row_high(const MxAttnArgs& a, const MxRows& r,
 
 template <MxPart PART>
 __device__ __forceinline__ int mx_row_low(const MxAttnArgs& a, const MxRows& r, int i) {
-  return PART == kMxWhole ? mx_low(a, r.back + i) : r.from;
+  return PART == kMxWhole ? mx_low(a, r.back + i) : PART == kMxThrough ? 0 : r.from;
 }
 
 // the block table's row of the sequence or group

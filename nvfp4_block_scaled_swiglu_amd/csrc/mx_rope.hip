@@ -91,21 +91,6 @@ __device__ __forceinline__ T head_sum(T x) {
   return x;
 }
 
-// The last sequence that starts at or before the row, 64 candidates at a time (a binary
-// search is a load's latency for each factor of two).
-__device__ __forceinline__ int sequence_of(const MxBatch& b, int64_t row, int lane) {
-  int lo = 0, n = b.batch;
-  while (n > 1) {
-    const int step = (n + 63) >> 6, i = lane * step;
-    const bool at = i < n && b.cu_seqlens[lo + i] <= row;
-    const int below = __popcll(__ballot(at));
-    const int skip = below > 0 ? (below - 1) * step : 0;
-    lo += skip;
-    n = n - skip < step ? n - skip : step;
-  }
-  return lo;
-}
-
 // 16 consecutive elements a lane into the cache
 template <int D>
 __device__ __forceinline__ void put(const Sixteen& x, uint8_t* codes, uint8_t* scales, int64_t row, int sub, bool there) {
@@ -167,7 +152,7 @@ __global__ __launch_bounds__(64 * kWaves) void mx_rope_kernel(MxRopeArgs a) {
   int pos = 0;
   int64_t page = -1;
   if (APPEND) {
-    const int seq = sequence_of(a.b, token, lane);
+    const int seq = mx_last(a.b.batch, [&](int i) { return a.b.cu_seqlens[i] <= token; });
     const int64_t r0 = mx_row_start(a.b, seq), r1 = mx_row_start(a.b, seq + 1);
     if (token < r0 || token >= r1) return;  // of no sequence
     pos = mx_seq_len(a.b, seq) - (int)(r1 - token);

@@ -114,8 +114,8 @@ def test_attention_prefix(kw, status):
 
 
 def test_prefix_workspace():
-    """Two pieces at least of 64 + 2 floats a row and head; none without rows; that of mxfp4_attention without groups."""
-    assert prefix({})[1] == 2 * 8 * 4 * 66 * 4
+    """Two pieces at least of 64 + 2 floats a row and head, and a word a row; none without rows; that of mxfp4_attention without groups."""
+    assert prefix({})[1] == 2 * 8 * 4 * 66 * 4 + 8 * 4
     assert prefix(dict(b_tokens=0))[1] == 0
     assert prefix(dict(mp=1 << 17))[1] > prefix({})[1]
     c, b = structs({})
