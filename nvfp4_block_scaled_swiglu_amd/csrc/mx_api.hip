@@ -277,10 +277,12 @@ int check_prefix(const mxfp4_cache* cache, const mxfp4_batch* batch, const mxfp4
   }
   *x = nvfp4::MxPrefix{prefix->block_table_dev, prefix->lens_dev, prefix->group_starts_dev, prefix->table_stride,
                        (int)prefix->groups, (int)prefix->max_pages};
-  if (prefix->groups > 0)
-    *plan = nvfp4::mx_prefix_plan(b->tokens, b->batch, prefix->groups, heads, c->kv_heads, c->head_dim, max_prefix, max_own);
+  constexpr int64_t most = 1 << 30;  // no sequence is longer
+  if (prefix->groups > 0 && b->batch > 0 && b->tokens > 0)
+    *plan = nvfp4::mx_prefix_plan(b->tokens, b->batch, prefix->groups, heads, c->kv_heads, c->head_dim,
+                                  nvfp4::mx_least(max_prefix, most), nvfp4::mx_least(max_own, most));
   else
-    plan->own = whole;
+    *plan = nvfp4::MxPrefixPlan{whole, whole, false};
   return NVFP4_OK;
 }
 

@@ -133,21 +133,43 @@ struct MxPrefixPlan {
   bool through;  // no parts: each sequence's rows over all of their tokens, by own (prompt form)
 };
 
+// Through: rows that fill the prompt form's tiles of 128 sequence by sequence save little by filling
+// them group by group, and pieces cost their way to memory and back, about what a tile takes
+// for 800 tokens. 8 sequences of 288 to 512 rows x 7 heads behind 6,144 tokens: 651 us, in parts 664.
+//
+// Pieces, of the prefix: in the prompt form a workgroup takes 1.3 us for a tile of 64 tokens alone on
+// its CU, 2.1 beside another, and 6 to begin and end; so one a CU until that makes more than 9
+// tiles of its own, then two. (3,072 tiles in 240 workgroups 39 us, 504 41; 7,504 in 256 68, 512
+// 57; 750 in 256 29, 512 34.) In the few-rows form up to 1,024 workgroups of 512 tokens at least: 64 packed rows of 12
+// groups over 8,200 tokens 31 us, in 2,048 workgroups 39. Of the rest: 1,024 tokens at least, as its workgroups
+// run beside the prefix's: 16 sequences over 6,000 of their own 44 us, 256 tokens 57, 4,096 68.
 constexpr int kMxJoinTokens = 800;
+
+inline int64_t mx_least(int64_t a, int64_t b) { return a < b ? a : b; }
 
 inline MxPrefixPlan mx_prefix_plan(int64_t tokens, int64_t batch, int64_t groups, int64_t heads, int64_t kv_heads,
                                    int64_t head_dim, int64_t max_prefix, int64_t max_own) {
   MxPrefixPlan p;
+  groups = mx_least(groups, tokens);
   p.own = mx_attention_plan(tokens, batch, heads, kv_heads, head_dim, max_own, 0, 0);
-  p.prefix = mx_attention_plan(tokens, groups < tokens ? groups : tokens, heads, kv_heads, head_dim, max_prefix, 0, 0);
+  p.prefix = mx_attention_plan(tokens, groups, heads, kv_heads, head_dim, max_prefix, 0, 0);
   const int64_t rows = tokens * (heads / kv_heads);
-  const int64_t own_tiles = batch > 0 ? ((rows + batch - 1) / batch + 127) / 128 * batch : 0;
-  const int64_t prefix_tiles = ((rows + groups - 1) / groups + 127) / 128 * groups;
+  auto tiles = [&](int64_t sequences, int of) { return ((rows + sequences - 1) / sequences + of - 1) / of * sequences; };
+  const int64_t own_tiles = tiles(batch, 128), prefix_tiles = tiles(groups, p.prefix.few ? 16 * p.prefix.row_tiles : 128);
   p.through = !p.own.few && (own_tiles - prefix_tiles) * max_prefix <= kMxJoinTokens * own_tiles;
   if (p.through) p.own = mx_attention_plan(tokens, batch, heads, kv_heads, head_dim, max_prefix + max_own, 0, 0);
+  const int64_t units = prefix_tiles * kv_heads;
+  int64_t s;
+  if (p.prefix.few) {
+    s = mx_least(1024 / units, max_prefix / 512);
+  } else {
+    const int64_t steps = units * (max_prefix / 64) / 9, most = head_dim == 256 ? 256 : 512;
+    s = mx_least((steps < 256 ? 256 : mx_least(steps, most)) / units, max_prefix / 128);
+  }
+  p.prefix.splits = (int)mx_least(s < 1 ? 1 : s, kMxMostSplits / 2);
+  if (p.own.few) p.own.splits = (int)mx_least(p.own.splits, max_own < 2048 ? 1 : max_own / 1024);
+  p.own.splits = (int)mx_least(p.own.splits, kMxMostSplits / 2);
   p.prefix.mixed = p.own.mixed = 0;
-  if (p.prefix.splits > kMxMostSplits / 2) p.prefix.splits = kMxMostSplits / 2;
-  if (p.own.splits > kMxMostSplits / 2) p.own.splits = kMxMostSplits / 2;
   return p;
 }
 

@@ -25,58 +25,124 @@ __device__ __forceinline__ int pages_of(const MxPages& p, int len) {
 
 __device__ __forceinline__ bool is_page(const MxPages& p, int page) { return page >= 0 && page < p.num_pages; }
 
-// ---- free ----
-// A workgroup per listed slot. Entries are taken out by exchange, so that of two workgroups
-// with the same slot one lowers a page's count; either finds the slot's length as it was or
-// cut by the other, and what the other cut, the other takes out.
-__global__ __launch_bounds__(kThreads) void mx_pages_free_kernel(MxPages p, const int32_t* slots, const int32_t* keep) {
-  const int slot = slots[blockIdx.x];
-  if (slot < 0 || slot >= p.slots) return;
-  __shared__ int len_was;
-  if (threadIdx.x == 0) len_was = __hip_atomic_load(p.lens + slot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  __syncthreads();
-  const int len = len_was, left = keep && keep[blockIdx.x] > 0 ? keep[blockIdx.x] : 0;
-  if (left >= len) return;
-  int32_t* row = p.table + (int64_t)slot * p.stride;
-  const int end = pages_of(p, len);
-#pragma unroll 4
-  for (int e = pages_of(p, left) + threadIdx.x; e < end; e += kThreads) {
-    const int page = atomicExch(row + e, -1);
-    if (is_page(p, page)) atomicSub(p.refs + page, 1);
+constexpr int kTogether = 8;  // list entries of a workgroup
+
+// The entries of a workgroup of the list, and what the whole list says about them.
+struct Listed {
+  int slot[kTogether], other[kTogether];
+  int begin[kTogether], end[kTogether];  // entries of their rows to go through; end 0: none
+};
+
+// A page in as many consecutive rows gets one atomic for all of them: forks of one sequence,
+// which stand next to each other in lists, share most of their pages. (64 x 16 forks of 513 pages: 7 us,
+// with an atomic each 20.)
+__device__ __forceinline__ void count_runs(const MxPages& p, const int (&page)[kTogether], int by) {
+  int run = 0;
+#pragma unroll
+  for (int k = 0; k < kTogether; ++k) {
+    ++run;
+    if (k + 1 < kTogether && page[k + 1] == page[k]) continue;
+    if (is_page(p, page[k])) atomicAdd(p.refs + page[k], by * run);
+    run = 0;
   }
-  if (threadIdx.x == 0) atomicMin(p.lens + slot, left);
+}
+
+// ---- free ----
+// Of entries with the same slot the first does the work, down to the smallest number that one of them
+// keeps; nobody else looks at the slot.
+__global__ __launch_bounds__(1024) void mx_pages_free_kernel(MxPages p, const int32_t* slots, const int32_t* keep, int n) {
+  __shared__ Listed at;
+  const int first = blockIdx.x * kTogether;
+  if (threadIdx.x < kTogether) {
+    const int i = first + threadIdx.x, slot = i < n ? slots[i] : -1;
+    at.slot[threadIdx.x] = slot >= 0 && slot < p.slots ? slot : -1;
+    at.other[threadIdx.x] = i < n && keep && keep[i] > 0 ? keep[i] : 0;
+  }
+  __syncthreads();
+  int slot[kTogether];
+#pragma unroll
+  for (int k = 0; k < kTogether; ++k) slot[k] = at.slot[k];
+  __syncthreads();
+  for (int j = threadIdx.x; j < n; j += blockDim.x) {
+    const int other = slots[j];
+#pragma unroll
+    for (int k = 0; k < kTogether; ++k) {
+      if (other != slot[k] || j == first + k || slot[k] < 0) continue;
+      if (j < first + k) at.slot[k] = -1;
+      else atomicMin(at.other + k, keep && keep[j] > 0 ? keep[j] : 0);
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < kTogether) {
+    const int mine = at.slot[threadIdx.x], left = at.other[threadIdx.x];
+    const int len = mine >= 0 ? p.lens[mine] : 0;
+    at.begin[threadIdx.x] = pages_of(p, left);
+    at.end[threadIdx.x] = left < len ? pages_of(p, len) : 0;
+    if (left < len) p.lens[mine] = left;
+  }
+  __syncthreads();
+  int last = 0;
+#pragma unroll
+  for (int k = 0; k < kTogether; ++k) last = at.end[k] > last ? at.end[k] : last;
+  for (int e = threadIdx.x; e < last; e += blockDim.x) {
+    int page[kTogether];
+#pragma unroll
+    for (int k = 0; k < kTogether; ++k)
+      page[k] = e >= at.begin[k] && e < at.end[k] ? p.table[(int64_t)at.slot[k] * p.stride + e] : -1;
+#pragma unroll
+    for (int k = 0; k < kTogether; ++k)
+      if (e >= at.begin[k] && e < at.end[k]) p.table[(int64_t)at.slot[k] * p.stride + e] = -1;
+    count_runs(p, page, -1);
+  }
 }
 
 // ---- fork ----
-// A workgroup per pair. Whether a pair counts depends on the lists and on lengths that no
-// pair that counts writes.
-__global__ __launch_bounds__(kThreads) void mx_pages_fork_kernel(MxPages p, const int32_t* parents, const int32_t* children,
-                                                                 int n, int32_t* done) {
-  const int i = blockIdx.x, parent = parents[i], child = children[i];
-  bool bad = parent < 0 || parent >= p.slots || child < 0 || child >= p.slots;
-  for (int j = threadIdx.x; j < n; j += kThreads) {
+// Whether a pair counts depends on the lists, and on lengths that no pair that counts writes but
+// its own.
+__global__ __launch_bounds__(1024) void mx_pages_fork_kernel(MxPages p, const int32_t* parents, const int32_t* children,
+                                                             int n, int32_t* done) {
+  __shared__ Listed at;  // slot: the child, other: the parent
+  __shared__ int bad[kTogether];
+  const int first = blockIdx.x * kTogether;
+  if (threadIdx.x < kTogether) {
+    const int i = first + threadIdx.x, child = i < n ? children[i] : -1, parent = i < n ? parents[i] : -1;
+    at.slot[threadIdx.x] = child;
+    at.other[threadIdx.x] = parent;
+    bad[threadIdx.x] = child < 0 || child >= p.slots || parent < 0 || parent >= p.slots || p.lens[child] > 0;
+  }
+  __syncthreads();
+  int child[kTogether], parent[kTogether];
+#pragma unroll
+  for (int k = 0; k < kTogether; ++k) {
+    child[k] = at.slot[k];
+    parent[k] = at.other[k];
+  }
+  for (int j = threadIdx.x; j < n; j += blockDim.x) {
     const int other = children[j];
-    bad |= (j < i && other == child) || other == parent;
+#pragma unroll
+    for (int k = 0; k < kTogether; ++k)
+      if ((other == child[k] && j < first + k) || other == parent[k]) bad[k] = 1;
   }
-  if (!__syncthreads_or(bad)) bad = p.lens[child] > 0;
-  else bad = true;
-  // every thread has read the length before it is written
-  if (__syncthreads_or(bad)) {
-    if (threadIdx.x == 0) done[i] = 0;
-    return;
+  __syncthreads();
+  if (threadIdx.x < kTogether) {
+    const int i = first + threadIdx.x, no = bad[threadIdx.x];
+    const int len = no ? 0 : p.lens[at.other[threadIdx.x]];
+    at.end[threadIdx.x] = pages_of(p, len);
+    if (!no) p.lens[at.slot[threadIdx.x]] = len > 0 ? len : 0;
+    if (i < n) done[i] = !no;
   }
-  const int len = p.lens[parent], held = pages_of(p, len);
-  const int32_t* from = p.table + (int64_t)parent * p.stride;
-  int32_t* to = p.table + (int64_t)child * p.stride;
-#pragma unroll 4
-  for (int e = threadIdx.x; e < held; e += kThreads) {
-    const int page = from[e];
-    to[e] = page;
-    if (is_page(p, page)) atomicAdd(p.refs + page, 1);
-  }
-  if (threadIdx.x == 0) {
-    p.lens[child] = len;
-    done[i] = 1;
+  __syncthreads();
+  int last = 0;
+#pragma unroll
+  for (int k = 0; k < kTogether; ++k) last = at.end[k] > last ? at.end[k] : last;
+  for (int e = threadIdx.x; e < last; e += blockDim.x) {
+    int page[kTogether];
+#pragma unroll
+    for (int k = 0; k < kTogether; ++k) page[k] = e < at.end[k] ? p.table[(int64_t)parent[k] * p.stride + e] : -1;
+#pragma unroll
+    for (int k = 0; k < kTogether; ++k)
+      if (e < at.end[k]) p.table[(int64_t)child[k] * p.stride + e] = page[k];
+    count_runs(p, page, 1);
   }
 }
 
@@ -105,22 +171,45 @@ __device__ __forceinline__ T scan(T x, T* sums /* [kPlan / 64] in LDS */, T& all
   return before + s - x;
 }
 
-// bit b of word w: page base + 64 w + b has a count above 0 (used) or not (free)
-__device__ __forceinline__ void fill_bits(const MxPages& p, int64_t base, bool used, uint64_t* bits) {
+__device__ __forceinline__ uint64_t below(int64_t n) {  // the lowest n bits
+  return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1;
+}
+
+// Bit b of word w: page 64 w + b has a count above 0. Up to kOneScan pages the planning workgroup
+// reads the counts itself, beyond that a launch over all CUs leaves it the words.
+constexpr int64_t kOneScan = 1 << 17;
+
+__device__ __forceinline__ uint64_t used_word(const MxPages& p, int64_t word) {
+  const int64_t page = word * 64 + (threadIdx.x & 63);
+  return __ballot(page < p.num_pages && p.refs[page] > 0);
+}
+
+__global__ __launch_bounds__(kThreads) void mx_pages_words_kernel(MxPages p, uint64_t* words) {
+  const int64_t word = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
+  const uint64_t b = used_word(p, word);
+  if ((threadIdx.x & 63) == 0 && word * 64 < p.num_pages) words[word] = b;
+}
+
+// the words of a segment in LDS, 0 behind the last page
+__device__ __forceinline__ void fill_bits(const MxPages& p, int64_t base, const uint64_t* ready, uint64_t* bits) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t left = p.num_pages - base;
   const int words = left >= kSegment ? kWords : (int)((left + 63) >> 6);
+  if (ready) {
+    for (int w = threadIdx.x; w < kWords; w += kPlan) bits[w] = w < words ? ready[base / 64 + w] : 0;
+    return;
+  }
   constexpr int kStep = kPlan / 64, kAhead = 8;
   for (int w = wave; w < words; w += kStep * kAhead) {
     int v[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int64_t page = base + (int64_t)(w + i * kStep) * 64 + lane;
-      v[i] = page < p.num_pages ? p.refs[page] : (used ? 0 : 1);
+      v[i] = p.refs[page < p.num_pages ? page : p.num_pages - 1];  // (a load under a condition waits for the one before)
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const uint64_t b = __ballot((v[i] > 0) == used);
+      const uint64_t b = __ballot(v[i] > 0) & below(left - (int64_t)(w + i * kStep) * 64);
       if (lane == 0 && w + i * kStep < words) bits[w + i * kStep] = b;
     }
   }
@@ -128,101 +217,34 @@ __device__ __forceinline__ void fill_bits(const MxPages& p, int64_t base, bool u
 }
 
 // ---- reserve ----
-// Two launches: one workgroup finds what each listed slot needs, where its share of the new
-// pages starts, and the lowest free pages; then a wave for each slot enters them.
-__global__ __launch_bounds__(kPlan) void mx_pages_plan_kernel(MxPages p, const int32_t* slots, const int32_t* lens, int n,
-                                                              MxReserveWork work) {
-  __shared__ uint64_t bits[kWords];
-  __shared__ int before[kWords];
-  __shared__ int64_t sums[kPlan / 64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  fill_bits(p, 0, false, bits);
-  // the first place in the list of each slot
-  for (int i = threadIdx.x; i < n; i += kPlan)
-    if (slots[i] >= 0 && slots[i] < p.slots) work.mark[slots[i]] = n;
-  __threadfence();
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kPlan)
-    if (slots[i] >= 0 && slots[i] < p.slots) atomicMin(work.mark + slots[i], i);
-  __threadfence();
-  __syncthreads();
-  int64_t total = 0;
-  for (int i0 = 0; i0 < n; i0 += kPlan) {
-    const int i = i0 + threadIdx.x;
-    int need = -1;  // not to be served
-    bool copies = false;
-    if (i < n) {
-      const int slot = slots[i], to = lens[i];
-      if (slot >= 0 && slot < p.slots &&
-          __hip_atomic_load(work.mark + slot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == i) {
-        const int len = p.lens[slot] > 0 ? p.lens[slot] : 0, have = pages_of(p, len);
-        if (to >= len && (int64_t)to <= (int64_t)p.max_pages << p.page_shift) {
-          if (to > len && (len & ((1 << p.page_shift) - 1)) != 0) {
-            const int last = p.table[(int64_t)slot * p.stride + have - 1];
-            copies = is_page(p, last) && p.refs[last] > 1;
-          }
-          need = pages_of(p, to) - have + (copies ? 1 : 0);
-        }
-      }
-    }
-    int64_t all;
-    const int64_t start = total + scan<int64_t>(need > 0 ? need : 0, sums, all);
-    if (i < n) work.plan[i] = make_int2(start < p.num_pages ? (int)start : (int)p.num_pages, need < 0 ? -1 : 2 * need + copies);
-    total += all;
-  }
-  const int64_t most = total < p.num_pages ? total : p.num_pages;
-  int64_t found = 0;
-  for (int64_t base = 0; found < most && base < p.num_pages; base += kSegment) {
-    if (base > 0) {
-      __syncthreads();
-      fill_bits(p, base, false, bits);
-    }
-    __syncthreads();
-    int count = 0;
-#pragma unroll
-    for (int j = 0; j < kEach; ++j) count += __popcll(bits[threadIdx.x * kEach + j]);
-    int64_t all;
-    int at = (int)scan<int64_t>(count, sums, all);
-#pragma unroll
-    for (int j = 0; j < kEach; ++j) {
-      before[threadIdx.x * kEach + j] = at;
-      at += __popcll(bits[threadIdx.x * kEach + j]);
-    }
-    __syncthreads();
-    const int64_t left = p.num_pages - base;
-    const int words = left >= kSegment ? kWords : (int)((left + 63) >> 6);
-    for (int w = wave; w < words; w += kPlan / 64) {
-      const uint64_t b = bits[w];
-      const int64_t k = found + before[w] + __popcll(b & ((1ull << lane) - 1));
-      if ((b >> lane & 1) != 0 && k < most) work.fresh[k] = (int)(base + (int64_t)w * 64 + lane);
-    }
-    found += all;
-  }
-  if (threadIdx.x == 0) *work.found = (int)(found < most ? found : most);
+// One workgroup finds what each listed slot needs, where its share of the new pages starts, and
+// the lowest free pages. A wave for each slot then enters them: for short lists a wave of the same
+// workgroup, otherwise of a launch of its own.
+constexpr int kOneLaunch = 128;
+
+// every access of the thread has been performed, atomics and stores in the L2
+__device__ __forceinline__ void drained() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0);
+  asm volatile("" ::: "memory");
 }
 
-__global__ __launch_bounds__(kThreads) void mx_pages_enter_kernel(MxPages p, const int32_t* slots, const int32_t* lens, int n,
-                                                                  int32_t* done, int32_t* src, int32_t* dst,
-                                                                  MxReserveWork work) {
-  const int lane = threadIdx.x & 63;
-  const int i = blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
-  if (i >= n) return;
-  const int2 plan = work.plan[i];
-  const int need = plan.y >> 1;
-  const bool served = plan.y >= 0 && (need == 0 || (int64_t)plan.x + need <= *work.found);
+// by the wave, for list entry i
+__device__ __forceinline__ void enter(const MxPages& p, int i, int2 plan, int found, int slot, int target, int len, int32_t* done,
+                                      int32_t* src, int32_t* dst, const int32_t* fresh) {
+  const int lane = threadIdx.x & 63, need = plan.y >> 1;
+  const bool served = plan.y >= 0 && (need == 0 || (int64_t)plan.x + need <= found);
   int from = -1, to = -1;
   if (served) {
-    const int slot = slots[i], target = lens[i];
-    const int len = p.lens[slot] > 0 ? p.lens[slot] : 0;
     int32_t* row = p.table + (int64_t)slot * p.stride;
     int have = pages_of(p, len);
     if (plan.y & 1) {
       --have;  // the last one too is new
       from = row[have];
-      to = work.fresh[plan.x];
+      to = fresh[plan.x];
     }
     for (int k = lane; k < need; k += 64) {
-      const int page = work.fresh[plan.x + k];
+      const int page = fresh[plan.x + k];
       row[have + k] = page;
       p.refs[page] = 1;
     }
@@ -238,15 +260,117 @@ __global__ __launch_bounds__(kThreads) void mx_pages_enter_kernel(MxPages p, con
   }
 }
 
-// ---- compact ----
-__device__ __forceinline__ uint64_t below(int64_t n) {  // the lowest n bits
-  return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1;
+__global__ __launch_bounds__(kPlan) void mx_pages_plan_kernel(MxPages p, const int32_t* slots, const int32_t* lens, int n,
+                                                              int32_t* done, int32_t* src, int32_t* dst, MxReserveWork work,
+                                                              const uint64_t* ready) {
+  __shared__ uint64_t bits[kWords];
+  __shared__ int before[kWords];
+  __shared__ int64_t sums[kPlan / 64];
+  __shared__ int2 plans[kOneLaunch];
+  __shared__ int4 asked[kOneLaunch];  // slot, length to be, length
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  // The first place in the list of each slot, by atomics: a store to be seen by them has to be in
+  // the L2, which waiting for it ensures; a fence would write back all of the L2 (2 us each).
+  for (int i = threadIdx.x; i < n; i += kPlan)
+    if (slots[i] >= 0 && slots[i] < p.slots)
+      __hip_atomic_store(work.mark + slots[i], n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  drained();
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kPlan)
+    if (slots[i] >= 0 && slots[i] < p.slots) atomicMin(work.mark + slots[i], i);
+  fill_bits(p, 0, ready, bits);
+  drained();
+  __syncthreads();
+  int64_t total = 0;
+  for (int i0 = 0; i0 < n; i0 += kPlan) {
+    const int i = i0 + threadIdx.x;
+    int need = -1;  // not to be served
+    bool copies = false;
+    int slot = -1, to = 0, len = 0;
+    if (i < n) {
+      slot = slots[i];
+      to = lens[i];
+      if (slot >= 0 && slot < p.slots) {
+        const int first = __hip_atomic_load(work.mark + slot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        len = p.lens[slot] > 0 ? p.lens[slot] : 0;
+        const int have = pages_of(p, len);
+        if (first == i && to >= len && (int64_t)to <= (int64_t)p.max_pages << p.page_shift) {
+          if (to > len && (len & ((1 << p.page_shift) - 1)) != 0) {
+            const int last = p.table[(int64_t)slot * p.stride + have - 1];
+            copies = is_page(p, last) && p.refs[last] > 1;
+          }
+          need = pages_of(p, to) - have + (copies ? 1 : 0);
+        }
+      }
+    }
+    int64_t all;
+    const int64_t start = total + scan<int64_t>(need > 0 ? need : 0, sums, all);
+    const int2 plan = make_int2(start < p.num_pages ? (int)start : (int)p.num_pages, need < 0 ? -1 : 2 * need + copies);
+    if (n <= kOneLaunch && i < n) {
+      plans[i] = plan;
+      asked[i] = make_int4(slot, to, len, 0);
+    } else if (i < n) {
+      work.plan[i] = plan;
+    }
+    total += all;
+  }
+  const int64_t most = total < p.num_pages ? total : p.num_pages;
+  int64_t found = 0;
+  for (int64_t base = 0; found < most && base < p.num_pages; base += kSegment) {
+    if (base > 0) {
+      __syncthreads();
+      fill_bits(p, base, ready, bits);
+      __syncthreads();
+    }
+    const int64_t left = p.num_pages - base;
+    const int words = left >= kSegment ? kWords : (int)((left + 63) >> 6);
+    int count = 0;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const int w = threadIdx.x * kEach + j;
+      count += __popcll(~bits[w] & below(left - (int64_t)w * 64));
+    }
+    int all;
+    int at = scan<int>(count, (int*)sums, all);
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const int w = threadIdx.x * kEach + j;
+      before[w] = at;
+      at += __popcll(~bits[w] & below(left - (int64_t)w * 64));
+    }
+    __syncthreads();
+    for (int w = wave; w < words; w += kPlan / 64) {
+      const uint64_t b = ~bits[w] & below(left - (int64_t)w * 64);
+      const int64_t k = found + before[w] + __popcll(b & below(lane));
+      if (found + before[w] >= most) break;
+      if ((b >> lane & 1) != 0 && k < most) work.fresh[k] = (int)(base + (int64_t)w * 64 + lane);
+    }
+    found += all;
+  }
+  found = found < most ? found : most;
+  if (threadIdx.x == 0) *work.found = (int)found;
+  if (n > kOneLaunch) return;
+  __syncthreads();
+  for (int i = wave; i < n; i += kPlan / 64)
+    enter(p, i, plans[i], (int)found, asked[i].x, asked[i].y, asked[i].z, done, src, dst, work.fresh);
 }
 
+__global__ __launch_bounds__(kThreads) void mx_pages_enter_kernel(MxPages p, const int32_t* slots, const int32_t* lens, int n,
+                                                                  int32_t* done, int32_t* src, int32_t* dst,
+                                                                  MxReserveWork work) {
+  const int i = blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
+  if (i >= n) return;
+  const int slot = slots[i];
+  const int2 plan = work.plan[i];
+  const int len = plan.y >= 0 && p.lens[slot] > 0 ? p.lens[slot] : 0;
+  enter(p, i, plan, *work.found, slot, lens[i], len, done, src, dst, work.fresh);
+}
+
+// ---- compact ----
 // With u pages in use, those at u and above move into the free ones below it, k-th to k-th.
 // One workgroup numbers both; then the tables are rewritten.
 __global__ __launch_bounds__(kPlan) void mx_pages_moves_kernel(MxPages p, int32_t* src, int32_t* dst, int32_t* used,
-                                                               int32_t* rank, int32_t* counts) {
+                                                               int32_t* rank, int32_t* counts, const uint64_t* ready) {
   __shared__ uint64_t bits[kWords];
   __shared__ int before[kWords];
   __shared__ int64_t sums[kPlan / 64];
@@ -254,7 +378,7 @@ __global__ __launch_bounds__(kPlan) void mx_pages_moves_kernel(MxPages p, int32_
   int64_t u = 0, all;
   for (int64_t base = 0; base < p.num_pages; base += kSegment) {
     __syncthreads();
-    fill_bits(p, base, true, bits);
+    fill_bits(p, base, ready, bits);
     __syncthreads();
     int count = 0;
 #pragma unroll
@@ -269,7 +393,7 @@ __global__ __launch_bounds__(kPlan) void mx_pages_moves_kernel(MxPages p, int32_
   for (int64_t base = 0; base < p.num_pages; base += kSegment) {
     if (p.num_pages > kSegment) {  // else they are there
       __syncthreads();
-      fill_bits(p, base, true, bits);
+      fill_bits(p, base, ready, bits);
       __syncthreads();
     }
     int nh[kEach], nm[kEach], h = 0, m = 0;
@@ -295,13 +419,12 @@ __global__ __launch_bounds__(kPlan) void mx_pages_moves_kernel(MxPages p, int32_
     const int64_t left = p.num_pages - base;
     const int words = left >= kSegment ? kWords : (int)((left + 63) >> 6);
     for (int i = wave; i < words; i += kPlan / 64) {
-      const uint64_t w = bits[i], low = below(u - base - (int64_t)i * 64), upto = (1ull << lane) - 1;
+      const uint64_t w = bits[i], low = below(u - base - (int64_t)i * 64), upto = below(lane);
       const int64_t page = base + (int64_t)i * 64 + lane;
       if ((~w & low) >> lane & 1) dst[holes + before[i] + __popcll(~w & low & upto)] = (int)page;
       if ((w & ~low) >> lane & 1) {
         const int64_t k = movers + (low == 0 ? before[i] : 0) + __popcll(w & ~low & upto);
         src[k] = (int)page;
-        counts[k] = p.refs[page];
         rank[page] = (int)k;
       }
     }
@@ -309,6 +432,18 @@ __global__ __launch_bounds__(kPlan) void mx_pages_moves_kernel(MxPages p, int32_
     movers += all & 0xFFFFFFFF;
   }
   for (int64_t k = movers + threadIdx.x; k < p.num_pages / 2; k += kPlan) src[k] = dst[k] = -1;
+  __syncthreads();
+  constexpr int kAhead = 4;  // the movers' counts: two loads each, of four at a time
+  for (int64_t k0 = threadIdx.x; k0 < movers; k0 += kPlan * kAhead) {
+    int c[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) c[i] = k0 + i * kPlan < movers ? src[k0 + i * kPlan] : 0;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) c[i] = p.refs[c[i]];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (k0 + i * kPlan < movers) counts[k0 + i * kPlan] = c[i];
+  }
 }
 
 // One thread for each count and each entry. A count is read where it is written, or from the
@@ -403,27 +538,57 @@ __global__ __launch_bounds__(kThreads) void mx_cache_copy_kernel(CopyArgs a) {
 
 }  // namespace
 
+// threads for rows of so many entries
+static int row_threads(const MxPages& p) { return p.max_pages > 512 ? 1024 : kThreads; }
+
+static unsigned list_groups(int n) { return (unsigned)((n + kTogether - 1) / kTogether); }
+
+// the words, for many pages; null: the planning workgroup reads the counts
+static hipError_t launch_words(const MxPages& p, uint64_t* words, const uint64_t** ready, hipStream_t stream) {
+  *ready = nullptr;
+  if (p.num_pages <= kOneScan) return hipSuccess;
+  *ready = words;
+  const int64_t n = (p.num_pages + 63) / 64;
+  constexpr int per = kThreads / 64;
+  mx_pages_words_kernel<<<(unsigned)((n + per - 1) / per), kThreads, 0, stream>>>(p, words);
+  return hipGetLastError();
+}
+
+static int64_t words_bytes(int64_t num_pages) { return num_pages <= kOneScan ? 0 : (num_pages + 63) / 64 * 8; }
+
+int64_t mx_reserve_bytes(int64_t n, int64_t slots, int64_t max_pages, int64_t num_pages) {
+  const int64_t most = n * (max_pages + 1), fresh = most < num_pages ? most : num_pages;
+  return (words_bytes(num_pages) + 8 * n + 16 + 4 * slots + 4 * fresh + 15) / 16 * 16;
+}
+
+int64_t mx_compact_bytes(int64_t num_pages) {
+  return (words_bytes(num_pages) + 4 * num_pages + 4 * (num_pages / 2) + 15) / 16 * 16;
+}
+
 hipError_t launch_mx_pages_free(const MxPages& p, const int32_t* slots, const int32_t* keep, int n, hipStream_t stream) {
-  mx_pages_free_kernel<<<n, kThreads, 0, stream>>>(p, slots, keep);
+  mx_pages_free_kernel<<<list_groups(n), row_threads(p), 0, stream>>>(p, slots, keep, n);
   return hipGetLastError();
 }
 
 hipError_t launch_mx_pages_fork(const MxPages& p, const int32_t* parents, const int32_t* children, int n, int32_t* done,
                                 hipStream_t stream) {
-  mx_pages_fork_kernel<<<n, kThreads, 0, stream>>>(p, parents, children, n, done);
+  mx_pages_fork_kernel<<<list_groups(n), row_threads(p), 0, stream>>>(p, parents, children, n, done);
   return hipGetLastError();
 }
 
 hipError_t launch_mx_pages_reserve(const MxPages& p, const int32_t* slots, const int32_t* lens, int n, int32_t* done,
                                    int32_t* src, int32_t* dst, void* workspace, hipStream_t stream) {
+  const uint64_t* ready;
+  hipError_t e = launch_words(p, (uint64_t*)workspace, &ready, stream);
+  if (e != hipSuccess) return e;
   MxReserveWork w;
-  w.plan = (int2*)workspace;
+  w.plan = (int2*)((uint8_t*)workspace + words_bytes(p.num_pages));
   w.found = (int32_t*)(w.plan + n);
   w.mark = w.found + 4;
   w.fresh = w.mark + p.slots;
-  mx_pages_plan_kernel<<<1, kPlan, 0, stream>>>(p, slots, lens, n, w);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  mx_pages_plan_kernel<<<1, kPlan, 0, stream>>>(p, slots, lens, n, done, src, dst, w, ready);
+  e = hipGetLastError();
+  if (e != hipSuccess || n <= kOneLaunch) return e;
   constexpr int per = kThreads / 64;
   mx_pages_enter_kernel<<<(n + per - 1) / per, kThreads, 0, stream>>>(p, slots, lens, n, done, src, dst, w);
   return hipGetLastError();
@@ -431,14 +596,17 @@ hipError_t launch_mx_pages_reserve(const MxPages& p, const int32_t* slots, const
 
 hipError_t launch_mx_pages_compact(const MxPages& p, int32_t* table_out, int64_t stride_out, int32_t* refs_out,
                                    int32_t* src, int32_t* dst, int32_t* used, void* workspace, hipStream_t stream) {
-  int32_t* rank = (int32_t*)workspace;
+  const uint64_t* ready;
+  hipError_t e = launch_words(p, (uint64_t*)workspace, &ready, stream);
+  if (e != hipSuccess) return e;
+  int32_t* rank = (int32_t*)((uint8_t*)workspace + words_bytes(p.num_pages));
   int32_t* counts = rank + p.num_pages;
-  mx_pages_moves_kernel<<<1, kPlan, 0, stream>>>(p, src, dst, used, rank, counts);
-  hipError_t e = hipGetLastError();
+  mx_pages_moves_kernel<<<1, kPlan, 0, stream>>>(p, src, dst, used, rank, counts, ready);
+  e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t count_groups = (p.num_pages + kThreads - 1) / kThreads, row_groups = (p.max_pages + kThreads - 1) / kThreads;
   mx_pages_rewrite_kernel<<<(unsigned)(count_groups + p.slots * row_groups), kThreads, 0, stream>>>(
-      p, table_out, stride_out, refs_out, src, dst, used, rank, counts, count_groups, row_groups > 0 ? row_groups : 1);
+      p, table_out, stride_out, refs_out, src, dst, used, rank, counts, count_groups, row_groups);
   return hipGetLastError();
 }
 

@@ -16,7 +16,8 @@ struct MxPages {
 
 constexpr int64_t kMxMostListed = 1 << 16;
 
-// workspace of a reserve: marks [slots], then per listed slot {start, need}, the pages found, and them
+// workspace of a reserve: by slot its first place in the list; by listed slot where its pages start among
+// the new ones and twice their number (one more if its last page is copied, -1: not served); the new pages
 struct MxReserveWork {
   int32_t* mark;
   int2* plan;
@@ -24,17 +25,9 @@ struct MxReserveWork {
   int32_t* fresh;
 };
 
-inline int64_t mx_reserve_fresh(int64_t n, int64_t max_pages, int64_t num_pages) {
-  const int64_t most = n * (max_pages + 1);
-  return most < num_pages ? most : num_pages;
-}
-
-inline int64_t mx_reserve_bytes(int64_t n, int64_t slots, int64_t max_pages, int64_t num_pages) {
-  return (8 * n + 16 + 4 * slots + 4 * mx_reserve_fresh(n, max_pages, num_pages) + 15) / 16 * 16;
-}
-
-// workspace of a compaction: rank of each mover, and the movers' counts
-inline int64_t mx_compact_bytes(int64_t num_pages) { return (4 * num_pages + 4 * (num_pages / 2) + 15) / 16 * 16; }
+// workspaces
+int64_t mx_reserve_bytes(int64_t n, int64_t slots, int64_t max_pages, int64_t num_pages);
+int64_t mx_compact_bytes(int64_t num_pages);
 
 hipError_t launch_mx_pages_free(const MxPages& p, const int32_t* slots, const int32_t* keep, int n, hipStream_t stream);
 hipError_t launch_mx_pages_fork(const MxPages& p, const int32_t* parents, const int32_t* children, int n, int32_t* done,

@@ -33,6 +33,8 @@ import ctypes
 from dataclasses import dataclass
 from typing import Optional, Tuple
 
+import torch
+
 import nvfp4_block_scaled_swiglu_amd as nv
 
 _P = ctypes.c_void_p
@@ -125,8 +127,8 @@ def mxfp4_scale_bytes(rows: int, k: int) -> int:
 @dataclass
 class Mxfp4Tensor:
     """A quantized [rows, k] tensor as the library lays it out in device memory."""
-    qdata: "torch.Tensor"   # uint8 [rows, k/2]
-    scales: "torch.Tensor"  # uint8 [mxfp4_scale_bytes(rows, k)], 128x4-tiled
+    qdata: torch.Tensor   # uint8 [rows, k/2]
+    scales: torch.Tensor  # uint8 [mxfp4_scale_bytes(rows, k)], 128x4-tiled
     rows: int
     k: int
 
@@ -134,10 +136,10 @@ class Mxfp4Tensor:
 @dataclass
 class Mxfp4Cache:
     """A paged key/value cache: per page and kv head, page_size rows of codes and scales."""
-    k_codes: "torch.Tensor"   # uint8 [num_pages, kv_heads, page_size, head_dim / 2]
-    k_scales: "torch.Tensor"  # uint8 [num_pages, kv_heads, page_size, head_dim / 32]
-    v_codes: "torch.Tensor"
-    v_scales: "torch.Tensor"
+    k_codes: torch.Tensor   # uint8 [num_pages, kv_heads, page_size, head_dim / 2]
+    k_scales: torch.Tensor  # uint8 [num_pages, kv_heads, page_size, head_dim / 32]
+    v_codes: torch.Tensor
+    v_scales: torch.Tensor
 
     @property
     def num_pages(self) -> int:
@@ -157,7 +159,6 @@ class Mxfp4Cache:
 
 
 def empty_mxfp4(rows: int, k: int, device) -> Mxfp4Tensor:
-    import torch
     return Mxfp4Tensor(qdata=torch.empty((rows, k // 2), dtype=torch.uint8, device=device),
                        scales=torch.empty((max(0, _scale_bytes(rows, k)),), dtype=torch.uint8, device=device),
                        rows=rows, k=k)
@@ -165,7 +166,6 @@ def empty_mxfp4(rows: int, k: int, device) -> Mxfp4Tensor:
 
 def empty_mxfp4_cache(num_pages: int, page_size: int, kv_heads: int, head_dim: int, device) -> Mxfp4Cache:
     """A cache whose contents are undefined until they are appended."""
-    import torch
     shape = (num_pages, kv_heads, page_size)
     make = lambda n: torch.empty(shape + (n,), dtype=torch.uint8, device=device)  # noqa: E731
     return Mxfp4Cache(make(head_dim // 2), make(head_dim // 32), make(head_dim // 2), make(head_dim // 32))
@@ -174,7 +174,6 @@ def empty_mxfp4_cache(num_pages: int, page_size: int, kv_heads: int, head_dim: i
 # ---- checks and streams --------------------------------------------------------------------
 
 def _bf16(t, name: str, dim: int, shape=None):
-    import torch
     if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.dim() != dim or not t.is_cuda:
         raise ValueError(f"{name} must be a {dim}-D bfloat16 CUDA tensor")
     if t.stride(-1) != 1 and t.shape[-1] > 1:
@@ -185,7 +184,6 @@ def _bf16(t, name: str, dim: int, shape=None):
 
 
 def _buffer(t, name: str, size: int):
-    import torch
     if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8 or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous uint8 CUDA tensor")
     if t.numel() < size:
@@ -211,7 +209,6 @@ def _scale_bytes(rows: int, k: int) -> int:  # mxfp4_scale_bytes without the cal
 
 
 def _int32(t, name: str, dim: int):
-    import torch
     if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != dim or not t.is_cuda:
         raise ValueError(f"{name} must be a {dim}-D int32 CUDA tensor")
     if t.stride(-1) != 1 and t.shape[-1] > 1:
@@ -233,7 +230,6 @@ def _strides(t) -> Tuple[int, int]:
 
 def _current_stream(index: int) -> int:
     """The handle of a device's current stream, without the object around it where torch has it so."""
-    import torch
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     return raw(index) if raw is not None else int(torch.cuda.current_stream(index).cuda_stream)
 
@@ -244,7 +240,6 @@ class _On:
     __slots__ = ("device", "handle", "stack", "side")
 
     def __init__(self, stream, *tensors):
-        import torch
         index = tensors[0].get_device()
         for t in tensors:
             if t.get_device() != index:
@@ -325,7 +320,6 @@ def mxfp4_quantize_swiglu(gate, up, out: Optional[Mxfp4Tensor] = None, stream=No
 
 def mxfp4_dequantize(t: Mxfp4Tensor, out=None, stream=None, strict: Optional[bool] = None):
     """The bf16 [rows, k] values of a quantized tensor (exact)."""
-    import torch
     _packed(t, "t")
     with _On(stream, t.qdata, t.scales) as on:
         if out is None:
@@ -344,7 +338,6 @@ def mxfp4_dequantize(t: Mxfp4Tensor, out=None, stream=None, strict: Optional[boo
 
 def mxfp4_gemm_bf16out(a: Mxfp4Tensor, w: Mxfp4Tensor, out=None, stream=None, strict: Optional[bool] = None):
     """D[m, n] = RN_bf16(sum_k A[m, k] W[n, k]) of a [m, k] and w [n, k], FP32 accumulation."""
-    import torch
     _packed(a, "a")
     _packed(w, "w")
     if a.k != w.k:
@@ -368,7 +361,6 @@ def mxfp4_gemm_bf16out(a: Mxfp4Tensor, w: Mxfp4Tensor, out=None, stream=None, st
 
 def _cache(c: Mxfp4Cache):
     """The cache's C form and its tensors."""
-    import torch
     if not isinstance(c, Mxfp4Cache):
         raise ValueError("cache must be an Mxfp4Cache")
     kc, ks, vc, vs = tensors = (c.k_codes, c.k_scales, c.v_codes, c.v_scales)
@@ -417,7 +409,6 @@ def mxfp4_cache_read(cache: Mxfp4Cache, block_table, seq_lens, cu_seqlens, token
                      strict: Optional[bool] = None):
     """(k, v), each bf16 [tokens, kv_heads, head_dim]: the values of the rows' positions, the
     last cu_seqlens[b + 1] - cu_seqlens[b] tokens of each sequence. out: such a pair."""
-    import torch
     c, ct = _cache(cache)
     b, bt = _batch(block_table, seq_lens, cu_seqlens, tokens)
     shape = (tokens, c.kv_heads, c.head_dim)
@@ -453,7 +444,6 @@ def mxfp4_attention(q, cache: Mxfp4Cache, block_table, seq_lens, cu_seqlens, sca
     decides how the work is split. workspace: a uint8 tensor of at least
     mxfp4_attention_workspace_bytes(...) bytes, allocated by default. Rows that see nothing give
     zeros; rows behind the last sequence keep what out held."""
-    import torch
     c, ct = _cache(cache)
     _bf16(q, "q", 3)
     tokens, heads, dim = q.shape
@@ -537,7 +527,6 @@ def mxfp4_attention_prefix(q, cache: Mxfp4Cache, block_table, seq_lens, cu_seqle
     longest prefix, and the most tokens of a sequence behind its own, as far as known (by default
     what the tables could hold); they decide how the work is split. workspace: a uint8 tensor of at least
     mxfp4_attention_prefix_workspace_bytes(...) bytes, allocated by default."""
-    import torch
     c, ct = _cache(cache)
     _bf16(q, "q", 3)
     tokens, heads, dim = q.shape

@@ -10,6 +10,8 @@ from __future__ import annotations
 from dataclasses import dataclass
 from typing import Optional
 
+import torch
+
 import nvfp4_block_scaled_swiglu_amd as nv
 
 from .mxfp4 import Mxfp4Cache, _buffer, _cache, _CPages, _int32, _On
@@ -19,9 +21,9 @@ from .mxfp4 import Mxfp4Cache, _buffer, _cache, _CPages, _int32, _On
 class Mxfp4Pages:
     """Sequences in slots and the pages that they hold: the first ceil(length / page_size) entries
     of a slot's row."""
-    block_table: "torch.Tensor"  # int32 [slots, max_pages]
-    seq_lens: "torch.Tensor"     # int32 [slots]
-    refs: "torch.Tensor"         # int32 [num_pages] entries that hold each page; below 1: free
+    block_table: torch.Tensor  # int32 [slots, max_pages]
+    seq_lens: torch.Tensor     # int32 [slots]
+    refs: torch.Tensor         # int32 [num_pages] entries that hold each page; below 1: free
     page_size: int
 
     @property
@@ -31,7 +33,6 @@ class Mxfp4Pages:
 
 def empty_mxfp4_pages(slots: int, max_pages: int, num_pages: int, page_size: int, device) -> Mxfp4Pages:
     """Empty sequences, every page free."""
-    import torch
     return Mxfp4Pages(torch.full((slots, max_pages), -1, dtype=torch.int32, device=device),
                       torch.zeros((slots,), dtype=torch.int32, device=device),
                       torch.zeros((num_pages,), dtype=torch.int32, device=device), page_size)
@@ -61,7 +62,6 @@ def _lists(first, name: str, second=None, other: str = ""):
 
 def _workspace(on: _On, workspace, size: int):
     """(pointer, bytes) of the caller's workspace or one of `size` bytes, and what keeps it."""
-    import torch
     if workspace is None:
         workspace = torch.empty((max(0, size),), dtype=torch.uint8, device=on.device)
     elif _buffer(workspace, "workspace", 0).device != on.device:
@@ -86,7 +86,6 @@ def mxfp4_pages_free(pages: Mxfp4Pages, slots, keep=None, stream=None, strict: O
 def mxfp4_pages_fork(pages: Mxfp4Pages, parents, children, stream=None, strict: Optional[bool] = None):
     """Make each empty slot children[i] a copy of sequence parents[i] (int32 [n] both), sharing its
     pages. Returns int32 [n]: 1 where that was done."""
-    import torch
     p, pt = _pages(pages)
     n = _lists(parents, "parents", children, "children")
     with _On(stream, *pt, parents, children) as on:
@@ -114,7 +113,6 @@ def mxfp4_pages_reserve(pages: Mxfp4Pages, slots, lens, workspace=None, stream=N
     which others hold the beginning too, has to be copied to dst[i] in every cache
     (mxfp4_cache_copy; -1: nothing to copy) before the sequence's next token is written and before
     pages are given out again."""
-    import torch
     p, pt = _pages(pages)
     n = _lists(slots, "slots", lens, "lens")
     with _On(stream, *pt, slots, lens) as on:
@@ -136,7 +134,6 @@ def mxfp4_pages_compact(pages: Mxfp4Pages, out: Optional[Mxfp4Pages] = None, wor
     """Renumber the used pages so that they are the first ones. Returns (after, src, dst, used): the
     record after it (out, which may be `pages`; by default new, sharing the lengths), the moves for
     mxfp4_cache_copy (int32 [num_pages // 2], -1 behind the last), and how many pages are in use (int32 [1])."""
-    import torch
     p, pt = _pages(pages)
     with _On(stream, *pt) as on:
         made = out is None

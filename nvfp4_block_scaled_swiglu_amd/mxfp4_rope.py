@@ -9,6 +9,8 @@ from __future__ import annotations
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
+import torch
+
 import nvfp4_block_scaled_swiglu_amd as nv
 
 from .mxfp4 import (Mxfp4Cache, _batch, _bf16, _cache, _CNorm, _CRotation, _On, _strides)
@@ -19,8 +21,8 @@ class Mxfp4Rotation:
     """What turns the pairs of a head: of the first 2 * len(freqs) elements, pair j - elements
     (j, j + len(freqs)), interleaved (2 j, 2 j + 1) - turns by freqs[j] radians for each step of
     the position on axis axes[j]."""
-    freqs: "torch.Tensor"                    # float32 [rotary_dim / 2]
-    axes: Optional["torch.Tensor"] = None    # int32 [rotary_dim / 2]; None: axis 0
+    freqs: torch.Tensor                    # float32 [rotary_dim / 2]
+    axes: Optional[torch.Tensor] = None    # int32 [rotary_dim / 2]; None: axis 0
     axis_count: int = 1
     interleaved: bool = False
 
@@ -30,7 +32,6 @@ def mxfp4_rotation(rotary_dim: int, device, theta: float = 10000.0, sections: Op
     """The usual frequencies theta ** (-2 j / rotary_dim). sections: how many pairs each axis has, in
     order (a time, height and width axis, say; they add up to rotary_dim / 2); separate: the
     frequencies of an axis then run over its own pairs, theta ** (-i / pairs), i from 0."""
-    import torch
     pairs = rotary_dim // 2
     sections = [pairs] if sections is None else [int(n) for n in sections]
     if rotary_dim <= 0 or rotary_dim % 2 or not sections or min(sections) < 0 or sum(sections) != pairs:
@@ -43,7 +44,6 @@ def mxfp4_rotation(rotary_dim: int, device, theta: float = 10000.0, sections: Op
 
 
 def _vector(t, name: str, dtype, size: Optional[int] = None):
-    import torch
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != 1 or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous 1-D {str(dtype).split('.')[-1]} CUDA tensor")
     if size is not None and t.shape[0] != size:
@@ -53,7 +53,6 @@ def _vector(t, name: str, dtype, size: Optional[int] = None):
 
 def _rotation(rotation: Optional[Mxfp4Rotation], positions, tokens: int, dim: int, cached: bool):
     """The rotation's C form and its tensors."""
-    import torch
     if rotation is None:
         if positions is not None:
             raise ValueError("positions without a rotation")
@@ -86,7 +85,6 @@ def _rotation(rotation: Optional[Mxfp4Rotation], positions, tokens: int, dim: in
 
 def _norm(weight, eps: Optional[float], name: str, dim: int):
     """The norm's C form and its tensors."""
-    import torch
     if eps is None:
         if weight is not None:
             raise ValueError(f"{name} without eps")
@@ -102,7 +100,6 @@ def mxfp4_norm_rope(x, rotation: Optional[Mxfp4Rotation] = None, positions=None,
     """Heads x (bf16 [tokens, heads, head_dim of 64, 128 or 256]) normed over head_dim (eps: not
     None; weight: bf16 [head_dim], or None for ones) and rotated at positions (int32 [tokens], or
     [tokens, axes] with one on each of the rotation's axes). out may be x."""
-    import torch
     tokens, heads, dim = _bf16(x, "x", 3).shape
     r, rt = _rotation(rotation, positions, tokens, dim, False)
     n, nt = _norm(weight, eps, "weight", dim)
@@ -128,7 +125,6 @@ def mxfp4_norm_rope_append(cache: Mxfp4Cache, q, k, v, block_table, seq_lens, cu
 
     positions: as in mxfp4_norm_rope; by default the rows' positions in their sequences. Rows
     behind the last sequence keep what out held."""
-    import torch
     c, ct = _cache(cache)
     tokens, heads, dim = _bf16(q, "q", 3).shape
     if dim != c.head_dim:

@@ -97,7 +97,7 @@ def test_too_few_pages(gpu):
     b.compact(True)
 
 
-@pytest.mark.parametrize("seed,slots,most,num,page", [(0, 20, 12, 100, 16), (1, 64, 30, 700, 64), (2, 5, 3, 9, 128), (3, 40, 70, 1500, 16)])
+@pytest.mark.parametrize("seed,slots,most,num,page", [(0, 20, 12, 100, 16), (1, 64, 30, 700, 64), (2, 5, 3, 9, 128), (3, 40, 70, 1500, 16), (4, 12, 700, 5000, 16), (5, 300, 9, 1800, 32)])
 def test_random_steps(gpu, seed, slots, most, num, page):
     rng = np.random.default_rng(seed)
     b = Both(gpu, slots, most, num, page)
