@@ -135,6 +135,27 @@ __device__ __forceinline__ int mx_last(int n, F at) {
   return __builtin_amdgcn_readfirstlane(lo);
 }
 
+// The sequence of a packed row, found by a whole wave: the row is one of its own if it lies in [r0, r1).
+// Up to 63 sequences cost one load's latency, their starts and lengths in the lanes.
+struct MxSequence {
+  int64_t r0, r1;
+  int seq, len;
+};
+
+__device__ __forceinline__ MxSequence mx_sequence(const MxBatch& b, int64_t row) {
+  if (b.batch >= 64) {
+    const int i = mx_last(b.batch, [&](int k) { return b.cu_seqlens[k] <= row; });
+    return MxSequence{mx_row_start(b, i), mx_row_start(b, i + 1), i, mx_seq_len(b, i)};
+  }
+  const int lane = __lane_id(), last = b.batch - 1;
+  const int64_t start = mx_row_start(b, lane < b.batch ? lane : b.batch);
+  const int len = mx_seq_len(b, lane < last ? lane : last);
+  const int below = __popcll(__ballot(lane < b.batch && start <= row));
+  const int i = below > 0 ? below - 1 : 0;
+  return MxSequence{__builtin_amdgcn_readlane((int)start, i), __builtin_amdgcn_readlane((int)start, i + 1), i,
+                    __builtin_amdgcn_readlane(len, i)};
+}
+
 // Where packed row `row` lives in the cache: its sequence is the last one that starts at
 // or before it. False for a row of no sequence; otherwise pos is its position (negative
 // if the sequence is shorter than its rows) and page its page, or -1 if that is not there.

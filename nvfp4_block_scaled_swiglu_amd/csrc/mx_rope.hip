@@ -30,8 +30,8 @@ constexpr int kWaves = 4;
 // what one wave has in LDS
 template <int D>
 struct WaveLds {
-  double2 turn[D / 2];   // cosine, sine of each pair
-  float2 turnf[D / 2];
+  double2 turn[D > 128 ? D / 2 : 64];   // cosine, sine of each pair
+  float2 turnf[D > 128 ? D / 2 : 64];
   uint16_t k[1024];      // keys on their way into blocks of 32 consecutive elements
 };
 
@@ -56,23 +56,27 @@ __device__ __forceinline__ double2 turn_of(int32_t position, float freq) {
   return make_double2(c, s);
 }
 
-// RN_bf16 of a double: by way of fp32, whose rounding must not make or hide a tie
-__device__ __forceinline__ uint32_t bf16_of(double x) {
-  const float f = (float)x;
-  uint32_t b = __float_as_uint(f);
-  if ((b & 0xFFFFu) == 0x8000u) {
-    const double d = fabs(x) - (double)fabsf(f);
-    b += d > 0.0 ? 1u : d < 0.0 ? -1u : 0u;
-  }
-  if (f != f) return 0x7FC0u | b >> 31 << 15;
-  return (b + 0x7FFFu + (b >> 16 & 1u)) >> 16;
-}
-
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   bf16x2_t c;
   c[0] = (__bf16)lo;
   c[1] = (__bf16)hi;
   return as_u32(c);
+}
+
+// RN_bf16 of two doubles, by way of fp32. That rounding must not make or hide a tie: where it ends on one,
+// the bit that it has dropped goes back in.
+__device__ __forceinline__ uint32_t pack2(double lo, double hi) {
+  float f[2] = {(float)lo, (float)hi};
+  const double x[2] = {lo, hi};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t b = __float_as_uint(f[i]);
+    if ((b & 0xFFFFu) == 0x8000u) {
+      const double d = fabs(x[i]) - (double)fabsf(f[i]);
+      f[i] = __uint_as_float(b + (d > 0.0 ? 1u : d < 0.0 ? -1u : 0u));
+    }
+  }
+  return pack2(f[0], f[1]);
 }
 
 struct Sixteen {
@@ -148,32 +152,43 @@ __global__ __launch_bounds__(64 * kWaves) void mx_rope_kernel(MxRopeArgs a) {
   };
   Sixteen next = fetch(part);
 
-  // ---- where the token belongs ----
-  int pos = 0;
-  int64_t page = -1;
-  if (APPEND) {
-    const int seq = mx_last(a.b.batch, [&](int i) { return a.b.cu_seqlens[i] <= token; });
-    const int64_t r0 = mx_row_start(a.b, seq), r1 = mx_row_start(a.b, seq + 1);
-    if (token < r0 || token >= r1) return;  // of no sequence
-    pos = mx_seq_len(a.b, seq) - (int)(r1 - token);
-    if (pos >= 0) {
-      const int64_t p = a.b.block_table[(int64_t)seq * a.b.table_stride + (pos >> a.b.page_shift)];
-      if (p >= 0 && p < a.b.num_pages) page = p;
-    }
-  }
-
-  // ---- the angles ----
-  if (part < qs + ks) {
-    for (int j = lane; j < a.rotary / 2; j += 64) {
-      int at = pos;
+  // ---- what the angles need ----
+  const bool angles = part < qs + ks;
+  constexpr int kPairs = D > 128 ? D / 128 : 1;  // of a lane
+  float freq[kPairs];
+  int at[kPairs];  // position
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) {
+    const int j = lane + 64 * i;
+    freq[i] = 0.0f;
+    at[i] = 0;
+    if (angles && j < a.rotary / 2) {
+      freq[i] = a.freqs[j];
       if (a.positions) {
         int axis = a.axes ? a.axes[j] : 0;
         axis = axis < 0 ? 0 : axis < a.axis_count ? axis : a.axis_count - 1;
-        at = a.positions[token * a.pos_token + axis * a.pos_axis];
+        at[i] = a.positions[token * a.pos_token + axis * a.pos_axis];
       }
-      const double2 t = turn_of(at, a.freqs[j]);
-      my.turn[j] = t;
-      my.turnf[j] = make_float2((float)t.x, (float)t.y);
+    }
+  }
+
+  // ---- where the token belongs ----
+  int pos = 0;
+  int64_t page = -1;  // as the table has it: it is looked at when the first key is written
+  if (APPEND) {
+    const MxSequence q = mx_sequence(a.b, token);
+    if (token < q.r0 || token >= q.r1) return;  // of no sequence
+    pos = q.len - (int)(q.r1 - token);
+    if (pos >= 0) page = a.b.block_table[(int64_t)q.seq * a.b.table_stride + (pos >> a.b.page_shift)];
+  }
+
+  // ---- the angles ----
+  if (angles && a.rotary > 0) {
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      const double2 t = turn_of(a.positions ? at[i] : pos, freq[i]);
+      my.turn[lane + 64 * i] = t;
+      my.turnf[lane + 64 * i] = make_float2((float)t.x, (float)t.y);
     }
     wave_sync();
   }
@@ -220,8 +235,10 @@ __global__ __launch_bounds__(64 * kWaves) void mx_rope_kernel(MxRopeArgs a) {
       }
       if (head < a.heads) {
         uint16_t* dst = a.out + token * a.out_token + head * a.out_head;
-        *(u32x4_t*)(dst + first) = u32x4_t{pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7])};
-        *(u32x4_t*)(dst + second) = u32x4_t{pack2(y[8], y[9]), pack2(y[10], y[11]), pack2(y[12], y[13]), pack2(y[14], y[15])};
+        const u32x4_t lo = {pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7])};
+        const u32x4_t hi = {pack2(y[8], y[9]), pack2(y[10], y[11]), pack2(y[12], y[13]), pack2(y[14], y[15])};
+        __builtin_nontemporal_store(lo, (u32x4_t*)(dst + first));
+        __builtin_nontemporal_store(hi, (u32x4_t*)(dst + second));
       }
       continue;
     }
@@ -230,19 +247,22 @@ __global__ __launch_bounds__(64 * kWaves) void mx_rope_kernel(MxRopeArgs a) {
     const int head = (s - (is_v ? qs + ks : qs)) * H + hl;
     Sixteen z = x;
     if (!is_v) {
-      double y[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) y[i] = x.at(i);
+      double y[16], r = 1.0;  // r after the rotation, which is linear
       if (a.k_norm.on) {
-        double sum = 0.0;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sum = fma(y[i], y[i], sum);
-        const double r = 1.0 / sqrt(head_sum<D>(sum) / D + a.k_norm.eps);
         Sixteen w;
         if (a.k_norm.weight) w = load(a.k_norm.weight, first, second);
         else w.w[0] = w.w[1] = u32x4_t{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+        double sum = 0.0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = y[i] * r * (double)w.at(i);
+        for (int i = 0; i < 16; ++i) {
+          const double u = x.at(i);
+          sum = fma(u, u, sum);
+          y[i] = u * (double)w.at(i);
+        }
+        r = rsqrt(head_sum<D>(sum) / D + a.k_norm.eps);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i] = x.at(i);
       }
       if (turns) {
 #pragma unroll
@@ -256,7 +276,7 @@ __global__ __launch_bounds__(64 * kWaves) void mx_rope_kernel(MxRopeArgs a) {
       }
       uint32_t w[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = bf16_of(y[2 * i]) | bf16_of(y[2 * i + 1]) << 16;
+      for (int i = 0; i < 8; ++i) w[i] = pack2(y[2 * i] * r, y[2 * i + 1] * r);
       z.w[0] = u32x4_t{w[0], w[1], w[2], w[3]};
       z.w[1] = u32x4_t{w[4], w[5], w[6], w[7]};
       if (!INTERLEAVED && a.rotary > 0) {
@@ -267,8 +287,10 @@ __global__ __launch_bounds__(64 * kWaves) void mx_rope_kernel(MxRopeArgs a) {
         wave_sync();
       }
     }
-    const int64_t row = (((page < 0 ? 0 : page) * a.c.kv_heads + head) << a.b.page_shift) + (pos & ((1 << a.b.page_shift) - 1));
-    put<D>(z, is_v ? a.c.v_codes : a.c.k_codes, is_v ? a.c.v_scales : a.c.k_scales, row, sub, page >= 0 && head < a.kv_heads);
+    const bool there = page >= 0 && page < a.b.num_pages;
+    const int64_t row = (((there ? page : 0) * a.c.kv_heads + head) << a.b.page_shift) + (pos & ((1 << a.b.page_shift) - 1));
+    put<D>(z, is_v ? a.c.v_codes : a.c.k_codes, is_v ? a.c.v_scales : a.c.k_scales, row, sub,
+           there && head < a.kv_heads);
   }
 }
 
