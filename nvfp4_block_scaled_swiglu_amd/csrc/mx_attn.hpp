@@ -158,17 +158,17 @@ inline MxPrefixPlan mx_prefix_plan(int64_t tokens, int64_t batch, int64_t groups
   const int64_t own_tiles = tiles(batch, 128), prefix_tiles = tiles(groups, p.prefix.few ? 16 * p.prefix.row_tiles : 128);
   p.through = !p.own.few && (own_tiles - prefix_tiles) * max_prefix <= kMxJoinTokens * own_tiles;
   if (p.through) p.own = mx_attention_plan(tokens, batch, heads, kv_heads, head_dim, max_prefix + max_own, 0, 0);
+  if (p.own.few) p.own.splits = (int)mx_least(p.own.splits, max_own < 2048 ? 1 : max_own / 1024);
+  p.own.splits = (int)mx_least(p.own.splits, kMxMostSplits / 2);
   const int64_t units = prefix_tiles * kv_heads;
   int64_t s;
   if (p.prefix.few) {
     s = mx_least(1024 / units, max_prefix / 512);
   } else {
     const int64_t steps = units * (max_prefix / 64) / 9, most = head_dim == 256 ? 256 : 512;
-    s = mx_least((steps < 256 ? 256 : mx_least(steps, most)) / units, max_prefix / 128);
+    s = mx_least(mx_least(steps < 256 ? 256 : steps, most) / units, max_prefix / 128);
   }
   p.prefix.splits = (int)mx_least(s < 1 ? 1 : s, kMxMostSplits / 2);
-  if (p.own.few) p.own.splits = (int)mx_least(p.own.splits, max_own < 2048 ? 1 : max_own / 1024);
-  p.own.splits = (int)mx_least(p.own.splits, kMxMostSplits / 2);
   p.prefix.mixed = p.own.mixed = 0;
   return p;
 }

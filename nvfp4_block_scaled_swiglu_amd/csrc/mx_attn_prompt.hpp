@@ -374,16 +374,17 @@ __device__ __forceinline__ void attend(const MxAttnArgs& a, const MxPlace& place
     auto clamp = [&](int i) __attribute__((always_inline)) { return span.at(i < end ? i : end - 1); };
     int tile = span.at(begin), next = clamp(begin + 1), far = clamp(begin + 2);
     Pages at = pages_of(tile), an = pages_of(next), af = pages_of(far);  // of the three tiles
+    Raw y;
     load_k(x, at);
     load_v(x, at);
+    load_k(y, an);
 #pragma unroll
     for (int d = 0; d < KE / 8; ++d) store_k(x, 0, d);
     mark_v(x, 0, tile, at);
 #pragma unroll
     for (int d = 0; d < VE / 2; ++d) store_v(x, 0, d);
-    load_k(x, an);
 #pragma unroll
-    for (int d = 0; d < KE / 8; ++d) store_k(x, 1, d);
+    for (int d = 0; d < KE / 8; ++d) store_k(y, 1, d);
     load_v(x, an);
     load_k(x, af);
     barrier();
