@@ -344,8 +344,18 @@ __device__ __forceinline__ void mx_rows_see(const MxAttnArgs& a, int i, int64_t 
 
 template <MxPart PART = kMxWhole>
 __device__ __forceinline__ MxRows mx_rows(const MxAttnArgs& a, int64_t tile, int rows) {
-  const int lo = mx_last(PART == kMxPrefix ? a.prefix.groups : a.b.batch,
-                         [&](int i) { return mx_part_start<PART>(a, i) * a.group / rows + i <= tile; });
+  int lo = 0;
+  if constexpr (PART == kMxWhole) {  // (mx_last here: the prompt form of 64 spills 12 registers for 9, 95 us for 91)
+    int hi = a.b.batch;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (mx_row_start(a.b, mid) * a.group / rows + mid <= tile) lo = mid;
+      else hi = mid;
+    }
+  } else {
+    lo = mx_last(PART == kMxPrefix ? a.prefix.groups : a.b.batch,
+                 [&](int i) { return mx_part_start<PART>(a, i) * a.group / rows + i <= tile; });
+  }
   MxRows r;
   const int64_t r1 = mx_part_start<PART>(a, lo + 1);
   r.seq = lo;
