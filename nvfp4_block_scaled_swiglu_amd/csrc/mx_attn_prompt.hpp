@@ -250,13 +250,15 @@ __device__ __forceinline__ void attend(const MxAttnArgs& a, const MxPlace& place
   };
   // (no short-circuits: selects, not branches around the accumulators)
   auto sees = [&](int t, uint32_t there, int group) __attribute__((always_inline)) {
-    return (t < high) & ((t >= low) | (t < sight.sinks)) & ((there >> group & 1u) != 0);
+    const bool page = (there >> group & 1u) != 0;
+    // (of a prefix rows see all; a lane without a row keeps to itself what it makes of it)
+    return PART == kMxPrefix ? page : (t < high) & ((t >= low) | (t < sight.sinks)) & page;
   };
   // register i of a half is its token 8 (i / 4) + 4 h + i % 4
   auto mask = [&](f32x16_t& x, int tile, int half, uint32_t there) __attribute__((always_inline)) {
     const int t0 = tile * kTile + half * 32;
-    if ((there >> (2 * half) & 3u) == 3u && t0 + 32 <= sight.high_min &&
-        (t0 >= sight.low_max || t0 + 32 <= sight.sinks))
+    if ((there >> (2 * half) & 3u) == 3u &&
+        (PART == kMxPrefix || (t0 + 32 <= sight.high_min && (t0 >= sight.low_max || t0 + 32 <= sight.sinks))))
       return;
 #pragma unroll
     for (int i = 0; i < 16; ++i)
