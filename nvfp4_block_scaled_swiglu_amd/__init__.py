@@ -143,7 +143,9 @@ def _call(name: str, *args, strict: Optional[bool] = None) -> bool:
     """Call entry point `name`; True on success. On failure raise (strict) or count a
     fallback and return False (non-strict)."""
     rc = getattr(lib(), name)(*args)
-    c = COUNTERS.setdefault(name, {"attempts": 0, "successes": 0, "fallbacks": 0, "failures": 0})
+    c = COUNTERS.get(name)
+    if c is None:
+        c = COUNTERS.setdefault(name, {"attempts": 0, "successes": 0, "fallbacks": 0, "failures": 0})
     c["attempts"] += 1
     if rc == NVFP4_OK:
         c["successes"] += 1

@@ -224,8 +224,8 @@ def _row_stride(t) -> int:
 
 def _strides(t) -> Tuple[int, int]:
     """(token, head) strides of [tokens, heads, dim]; those of single ones mean nothing."""
-    tokens, heads, dim = t.shape
-    return (t.stride(0) if tokens > 1 else 0, t.stride(1) if heads > 1 else dim)
+    shape, strides = t.shape, t.stride()
+    return (strides[0] if shape[0] > 1 else 0, strides[1] if shape[1] > 1 else shape[2])
 
 
 def _current_stream(index: int) -> int:

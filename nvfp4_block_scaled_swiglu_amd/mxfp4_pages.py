@@ -116,7 +116,7 @@ def mxfp4_pages_reserve(pages: Mxfp4Pages, slots, lens, workspace=None, stream=N
     p, pt = _pages(pages)
     n = _lists(slots, "slots", lens, "lens")
     with _On(stream, *pt, slots, lens) as on:
-        done, src, dst = torch.empty((3, n), dtype=torch.int32, device=on.device)
+        done, src, dst = torch.empty((3, n), dtype=torch.int32, device=on.device).unbind()
         workspace = _workspace(on, workspace, nv.lib().mxfp4_pages_reserve_workspace_bytes(p, n) if workspace is None else 0)
         if not nv._call("mxfp4_pages_reserve", p, slots.data_ptr(), lens.data_ptr(), n, done.data_ptr(), src.data_ptr(),
                         dst.data_ptr(), workspace.data_ptr(), workspace.numel(), on.handle, strict=strict):
@@ -150,7 +150,7 @@ def mxfp4_pages_compact(pages: Mxfp4Pages, out: Optional[Mxfp4Pages] = None, wor
         if not made:
             on.use(*ot)
         moves = torch.empty((2 * (p.num_pages // 2) + 1,), dtype=torch.int32, device=on.device)
-        src, dst, used = moves[:p.num_pages // 2], moves[p.num_pages // 2:-1], moves[-1:]
+        src, dst, used = moves.split((p.num_pages // 2, p.num_pages // 2, 1))
         workspace = _workspace(on, workspace, nv.lib().mxfp4_pages_compact_workspace_bytes(p) if workspace is None else 0)
         if not nv._call("mxfp4_pages_compact", p, o.block_table, o.table_stride, o.refs, src.data_ptr(), dst.data_ptr(),
                         used.data_ptr(), workspace.data_ptr(), workspace.numel(), on.handle, strict=strict):
