@@ -76,7 +76,7 @@ def test_values_at_the_edges_of_the_types(gpu):
     rot, freqs, which = rotation(gpu, 64)
     pos = np.array([[5], [123456]], np.int32)
     xd, pd = parity.to_device_bf16(bits, gpu), torch.from_numpy(pos).to(gpu)
-    for eps in (1e-6, 1e-30, 1e30):
+    for eps in (1e-6, 1e-30, 1e30, 5e-324):
         # (an infinite head: its norm is infinite, others 0, itself NaN, and its pair with it)
         check(nv.mxfp4_norm_rope(xd, rot, pd, eps=eps), bits, ref.turns(pos, freqs, which), eps=eps)
 
@@ -207,6 +207,30 @@ def test_append_without_change_is_the_plain_append(gpu):
         caches.append(c.cache)
     for n in ("k_codes", "k_scales", "v_codes", "v_scales"):
         assert torch.equal(getattr(caches[0], n), getattr(caches[1], n)), n
+
+
+def test_keys_at_the_edges_of_the_types(gpu):
+    """Through the append: keys of zeros, of numbers at either end of the range, with an infinity or a NaN."""
+    import nvfp4_block_scaled_swiglu_amd as nv
+    rng = np.random.default_rng(3)
+    x = rng.standard_normal((9, 1, 64))
+    for i, scale in enumerate([0.0, 1e-38, 1e-30, 1e-20, 1.0, 1e19, 1e30, 2.0 ** 125, 1.0]):
+        x[i] *= scale
+    bits = mx_ref.f64_to_bits(x)
+    bits[4, 0, 17], bits[8, 0, 3] = 0xFF80, 0x7FC0
+    rot, freqs, _ = rotation(gpu, 64)
+    rot.axes = None
+    d = parity.to_device_bf16(bits, gpu)
+    for eps in (1e-6, 1e-30, 1e30, 5e-324):
+        c = Case(gpu, [(9, 12)], dim=64, page=16, kv_heads=1)
+        nv.mxfp4_norm_rope_append(c.cache, d, d, d, c.table, c.seq, c.cu, rot, eps=eps)
+        k = nv.mxfp4_cache_read(c.cache, c.table, c.seq, c.cu, 9)[0].double().cpu().numpy()
+        y, _ = ref.norm_rope(mx_ref.bits_to_f64(bits), ref.turns(np.arange(3, 12)[:, None], freqs), eps=eps)
+        broken = [4, 8]
+        fine = [i for i in range(9) if i not in broken]
+        np.testing.assert_array_equal(k[fine], mx_ref.round_trip(mx_ref.f64_to_bits(y[fine])))
+        # the infinity: NaN for its block and its pair's; the NaN: for all of the head
+        assert np.isnan(k[8]).all() and np.isnan(k[4]).all()
 
 
 def test_rows_without_a_place(gpu):
