@@ -137,12 +137,14 @@ struct MxPrefixPlan {
 // them group by group, and pieces cost their way to memory and back, about what a tile takes
 // for 800 tokens. 8 sequences of 288 to 512 rows x 7 heads behind 6,144 tokens: 651 us, in parts 664.
 //
-// Pieces, of the prefix: in the prompt form a workgroup takes 1.3 us for a tile of 64 tokens alone on
-// its CU, 2.1 beside another, and 6 to begin and end; so one a CU until that makes more than 9
-// tiles of its own, then two. (3,072 tiles in 240 workgroups 39 us, 504 41; 7,504 in 256 68, 512
-// 57; 750 in 256 29, 512 34.) In the few-rows form up to 1,024 workgroups of 512 tokens at least: 64 packed rows of 12
-// groups over 8,200 tokens 31 us, in 2,048 workgroups 39. Of the rest: 1,024 tokens at least, as its workgroups
-// run beside the prefix's: 16 sequences over 6,000 of their own 44 us, 256 tokens 57, 4,096 68.
+// Pieces, of the prefix: in the prompt form a workgroup of 128 takes 1.3 us for a tile of 64 tokens alone on its CU,
+// 1.6 beside one of the rest, 2.1 beside another of the prefix, and 6 to begin and end; the rest needs 10 us
+// in what is free, and after the prefix where nothing is. So one a CU up to 19 tiles each, then two: 3,072 tiles in
+// 240 workgroups 28 us, 336 30, 456 33; 7,504 in 256 68 with the join, 512 57. Of 64 a CU has three, and 9 tiles
+// each are best up to two: 4,512 in 240 48 us, 480 36; 3,500 in 384 29, 512 32. In the few-rows form up to 1,024 workgroups of 512
+// tokens at least: 64 packed rows of 12 groups over 8,200 tokens 31 us, in 2,048 workgroups 39. Of the rest: 1,024 tokens at
+// least, as its workgroups run beside the prefix's: 16 sequences over 6,000 of their own 44 us, 256 tokens
+// 57, 4,096 68.
 constexpr int kMxJoinTokens = 800;
 
 inline int64_t mx_least(int64_t a, int64_t b) { return a < b ? a : b; }
@@ -165,8 +167,11 @@ inline MxPrefixPlan mx_prefix_plan(int64_t tokens, int64_t batch, int64_t groups
   if (p.prefix.few) {
     s = mx_least(1024 / units, max_prefix / 512);
   } else {
-    const int64_t steps = units * (max_prefix / 64) / 9, most = head_dim == 256 ? 256 : 512;
-    s = mx_least(mx_least(steps < 256 ? 256 : steps, most) / units, max_prefix / 128);
+    const int64_t steps = units * (max_prefix / 64);
+    int64_t most = 256;  // workgroups
+    if (head_dim == 64 && steps > 9 * 256) most = mx_least(steps / 9, 512);
+    if (head_dim == 128 && steps > 19 * 256) most = 512;
+    s = mx_least(most / units, max_prefix / 128);
   }
   p.prefix.splits = (int)mx_least(s < 1 ? 1 : s, kMxMostSplits / 2);
   p.prefix.mixed = p.own.mixed = 0;

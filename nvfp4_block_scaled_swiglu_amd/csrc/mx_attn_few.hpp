@@ -1,5 +1,5 @@
 // mx_attn_few.hpp - attention over a paged MXFP4 cache, for few rows of a sequence (gfx950):
-// single tokens of a decoding batch, a few drafted ones. Many rows: mx_attn_prompt.hip.
+// single tokens of a decoding batch, a few drafted ones. Many rows: mx_attn_prompt.hpp.
 //
 //   o[i, h] = sum_t softmax_t(scale * q[i, h] . k[t, h / g]) v[t, h / g]
 //

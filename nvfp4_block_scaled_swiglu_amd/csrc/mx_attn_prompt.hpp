@@ -37,7 +37,7 @@
 // of the weights as rounded for the product, two to an instruction (v_dot2_f32_bf16, fp32).
 //
 // Masks are put into S as -inf, only in halves that some row does not see whole. Arithmetic
-// is that of mx_attn.hip.
+// is that of mx_attn_few.hpp.
 #pragma once
 
 #include <type_traits>
