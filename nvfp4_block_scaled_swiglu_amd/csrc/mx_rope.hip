@@ -15,8 +15,13 @@
 //
 // A token's angles are the same for all of its heads: lane j finds cosine and sine of pair j
 // once, in fp64, and the wave keeps them in LDS. Queries are then fp32 throughout; keys
-// are fp64, because the step after their rounding to bf16 is one to 4 bits, where a last
-// bit that falls the other way can move the result by half of itself.
+// are fp64 (as fast here as unpacked fp32), because the step after their rounding to bf16 is one
+// to 4 bits, where a last bit that falls the other way can move the result by half of itself.
+//
+// Measured: 37,810 tokens, 56 heads of 128, three axes: 220 us, 4.9 TB/s (a large copy: 5.1 to 5.2). 32,765 tokens of 32
+// and 8 heads of 128 into the cache: 163 us, 4.3 TB/s; the queries alone take 107, the values' part of the cache 22 beside them
+// and the keys' 36, a third of it arithmetic. One token 4.4 us, 48 tokens 4.8. One wave to a token and no more: two make
+// it 185 us (the angles and the search twice), four tokens to a wave 196 (registers); loads two steps ahead change nothing.
 #include <cmath>
 
 #include "mx_rope.hpp"
@@ -237,6 +242,7 @@ __global__ __launch_bounds__(64 * kWaves) void mx_rope_kernel(MxRopeArgs a) {
         uint16_t* dst = a.out + token * a.out_token + head * a.out_head;
         const u32x4_t lo = {pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7])};
         const u32x4_t hi = {pack2(y[8], y[9]), pack2(y[10], y[11]), pack2(y[12], y[13]), pack2(y[14], y[15])};
+        // (past the caches: 32,765 tokens of 32 heads of 64 75 us, otherwise 97; such loads cost 8 %)
         __builtin_nontemporal_store(lo, (u32x4_t*)(dst + first));
         __builtin_nontemporal_store(hi, (u32x4_t*)(dst + second));
       }
