@@ -130,7 +130,7 @@ inline int64_t mx_part_bytes(const MxAttnPlan& p, int64_t tokens, int64_t batch,
 // A call with shared prefixes: what the groups' rows see of them, and the rest of the sequences.
 struct MxPrefixPlan {
   MxAttnPlan prefix, own;
-  bool through;  // no parts: each sequence's rows over all of their tokens, by own (prompt form)
+  bool through;  // no parts: each sequence's rows over all of their tokens, by own (prompt form); else own is few
 };
 
 // Through: rows that fill the prompt form's tiles of 128 sequence by sequence save little by filling
@@ -144,7 +144,8 @@ struct MxPrefixPlan {
 // each are best up to two: 4,512 in 240 48 us, 480 36; 3,500 in 384 29, 512 32. In the few-rows form up to 1,024 workgroups of 512
 // tokens at least: 64 packed rows of 12 groups over 8,200 tokens 31 us, in 2,048 workgroups 39. Of the rest: 1,024 tokens at
 // least, as its workgroups run beside the prefix's: 16 sequences over 6,000 of their own 44 us, 256 tokens
-// 57, 4,096 68.
+// 57, 4,096 68. The rest is always the few-rows form's, which has no tiles of 128 to fill: 16 sequences of 35 packed
+// rows behind 8,200 48 us, in the prompt form 55; of 112 over 4,000 of their own 85 for 97.
 constexpr int kMxJoinTokens = 800;
 
 inline int64_t mx_least(int64_t a, int64_t b) { return a < b ? a : b; }
@@ -153,15 +154,18 @@ inline MxPrefixPlan mx_prefix_plan(int64_t tokens, int64_t batch, int64_t groups
                                    int64_t head_dim, int64_t max_prefix, int64_t max_own) {
   MxPrefixPlan p;
   groups = mx_least(groups, tokens);
-  p.own = mx_attention_plan(tokens, batch, heads, kv_heads, head_dim, max_own, 0, 0);
   p.prefix = mx_attention_plan(tokens, groups, heads, kv_heads, head_dim, max_prefix, 0, 0);
   const int64_t rows = tokens * (heads / kv_heads);
   auto tiles = [&](int64_t sequences, int of) { return ((rows + sequences - 1) / sequences + of - 1) / of * sequences; };
   const int64_t own_tiles = tiles(batch, 128), prefix_tiles = tiles(groups, p.prefix.few ? 16 * p.prefix.row_tiles : 128);
+  p.own = mx_attention_plan(tokens, batch, heads, kv_heads, head_dim, max_prefix + max_own, 0, 0);
   p.through = !p.own.few && (own_tiles - prefix_tiles) * max_prefix <= kMxJoinTokens * own_tiles;
-  if (p.through) p.own = mx_attention_plan(tokens, batch, heads, kv_heads, head_dim, max_prefix + max_own, 0, 0);
-  if (p.own.few) p.own.splits = (int)mx_least(p.own.splits, max_own < 2048 ? 1 : max_own / 1024);
-  p.own.splits = (int)mx_least(p.own.splits, kMxMostSplits / 2);
+  if (!p.through) {
+    p.own.few = true;
+    p.own.row_tiles = head_dim == 64 && rows > 16 * batch ? 2 : 1;
+    const int64_t s = 2048 / (tiles(batch, 16 * p.own.row_tiles) * kv_heads);
+    p.own.splits = (int)mx_least(s < 1 ? 1 : s, max_own < 2048 ? 1 : mx_least(max_own / 1024, kMxMostSplits / 2));
+  }
   const int64_t units = prefix_tiles * kv_heads;
   int64_t s;
   if (p.prefix.few) {

@@ -104,9 +104,8 @@ hipError_t launch_dim(const MxAttnArgs& a, const MxPrefixPlan& plan, hipStream_t
   const int p = form(plan.prefix, D), o = form(plan.own, D);
   constexpr int T = D == 64 ? 2 : 1;
   hipError_t e;
-  if (o == 0) e = launch_both<D, 0, 0>(x, y, stream);  // (a group has a sequence's rows at least)
-  else if (o == 1) e = p == 0 ? launch_both<D, 0, 1>(x, y, stream)
-                              : p == 1 ? launch_both<D, 1, 1>(x, y, stream) : launch_both<D, T, 1>(x, y, stream);
+  if (o == 1) e = p == 0 ? launch_both<D, 0, 1>(x, y, stream)
+                         : p == 1 ? launch_both<D, 1, 1>(x, y, stream) : launch_both<D, T, 1>(x, y, stream);
   else e = p == 0 ? launch_both<D, 0, T>(x, y, stream) : launch_both<D, T, T>(x, y, stream);
   if (e != hipSuccess) return e;
   x.splits = pieces;
@@ -122,8 +121,7 @@ hipError_t setup_both() {
 template <int D>
 hipError_t setup_dim() {
   constexpr int T = D == 64 ? 2 : 1;
-  hipError_t e = setup_both<D, 0, 0>();
-  if (e == hipSuccess) e = setup_both<D, 0, 1>();
+  hipError_t e = setup_both<D, 0, 1>();
   if (e == hipSuccess) e = setup_both<D, 1, 1>();
   if (e == hipSuccess) e = setup_both<D, T, 1>();
   if (e == hipSuccess) e = setup_both<D, 0, T>();
