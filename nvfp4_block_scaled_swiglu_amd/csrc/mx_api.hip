@@ -256,10 +256,11 @@ int check_prefix(const mxfp4_cache* cache, const mxfp4_batch* batch, const mxfp4
                  int64_t max_prefix, int64_t max_own, nvfp4::MxCache* c, nvfp4::MxBatch* b, nvfp4::MxPrefix* x,
                  nvfp4::MxPrefixPlan* plan) {
   if (!prefix) return api_fail(NVFP4_ERR_INVALID_ARG, "null prefix");
+  if (max_prefix <= 0 || max_own <= 0)
+    return api_fail(NVFP4_ERR_INVALID_ARG, "max_prefix=%lld max_own=%lld", (long long)max_prefix, (long long)max_own);
   nvfp4::MxAttnPlan whole;
   const int rc = check_attention(cache, batch, heads, max_own, 0, 0, c, b, &whole);
   if (rc != NVFP4_OK) return rc;
-  if (max_prefix <= 0) return api_fail(NVFP4_ERR_INVALID_ARG, "max_prefix=%lld", (long long)max_prefix);
   if (prefix->groups < 0 || prefix->max_pages < 0 || prefix->table_stride < prefix->max_pages)
     return api_fail(NVFP4_ERR_INVALID_ARG, "bad prefix: %lld groups, %lld pages (stride %lld)", (long long)prefix->groups,
                     (long long)prefix->max_pages, (long long)prefix->table_stride);

@@ -145,8 +145,6 @@ def mxfp4_pages_compact(pages: Mxfp4Pages, out: Optional[Mxfp4Pages] = None, wor
             raise ValueError("out must be of the size of pages")
         if any(t.device != on.device for t in ot):
             raise ValueError("out must be on the device of pages")
-        if o.seq_lens != p.seq_lens:
-            out.seq_lens.copy_(pages.seq_lens)
         if not made:
             on.use(*ot)
         moves = torch.empty((2 * (p.num_pages // 2) + 1,), dtype=torch.int32, device=on.device)
@@ -155,6 +153,8 @@ def mxfp4_pages_compact(pages: Mxfp4Pages, out: Optional[Mxfp4Pages] = None, wor
         if not nv._call("mxfp4_pages_compact", p, o.block_table, o.table_stride, o.refs, src.data_ptr(), dst.data_ptr(),
                         used.data_ptr(), workspace.data_ptr(), workspace.numel(), on.handle, strict=strict):
             return None
+        if o.seq_lens != p.seq_lens:
+            out.seq_lens.copy_(pages.seq_lens)
     return out, src, dst, used
 
 

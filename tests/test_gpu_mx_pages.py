@@ -165,6 +165,24 @@ def test_strided_rows(gpu):
     assert bool((wide[:, :2] == 77).all()) and bool((wide[:, 7:] == 77).all())
 
 
+def test_compact_into_a_record(gpu):
+    """Of the caller's, with lengths of its own and wider rows; one of another size is refused."""
+    import torch
+    import nvfp4_block_scaled_swiglu_amd as nv
+    b = Both(gpu, 3, 4, 20, 16)
+    b.reserve([0, 1, 2], [60, 33, 20])
+    b.free([0])
+    wide = torch.full((3, 8), 77, dtype=torch.int32, device=gpu)
+    out = nv.Mxfp4Pages(wide[:, 1:5], torch.full((3,), 9, dtype=torch.int32, device=gpu), torch.full((20,), 5, dtype=torch.int32, device=gpu), 16)
+    assert nv.mxfp4_pages_compact(b.pages, out=out)[0] is out
+    b.check()
+    b.model.compact()
+    same(out, b.model)
+    assert bool((wide[:, :1] == 77).all()) and bool((wide[:, 5:] == 77).all())
+    with pytest.raises(ValueError):
+        nv.mxfp4_pages_compact(b.pages, out=nv.empty_mxfp4_pages(3, 4, 21, 16, gpu))
+
+
 def cache_of(gpu, pages, page, heads, dim, seed):
     import torch
     import nvfp4_block_scaled_swiglu_amd as nv
