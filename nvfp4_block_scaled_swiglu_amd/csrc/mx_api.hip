@@ -268,7 +268,7 @@ int check_prefix(const mxfp4_cache* cache, const mxfp4_batch* batch, const mxfp4
       prefix->max_pages << b->page_shift >= (int64_t)1 << 30)
     return api_fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "prefixes beyond 2^24 groups or 2^30 tokens");
   if (b->tokens * heads >= (int64_t)1 << 26 ||
-      (b->tokens * (heads / c->kv_heads) / 16 + prefix->groups) * c->kv_heads > kMostGroups)
+      (b->tokens * (heads / c->kv_heads) / 16 * 2 + b->batch + prefix->groups) * c->kv_heads > kMostGroups)
     return api_fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "too many rows and heads for one call");
   if (prefix->groups > 0 && b->batch > 0 && b->tokens > 0) {
     if (!prefix->lens_dev || !prefix->group_starts_dev || (prefix->max_pages > 0 && !prefix->block_table_dev))

@@ -150,9 +150,15 @@ constexpr int kMxJoinTokens = 800;
 
 inline int64_t mx_least(int64_t a, int64_t b) { return a < b ? a : b; }
 
+// row tiles of a launch, by their numbering (mx_rows)
+inline int64_t mx_part_tiles(int64_t packed, int64_t sequences, int rows) {
+  return (packed + rows - 1) / rows + sequences - 1;
+}
+
 inline MxPrefixPlan mx_prefix_plan(int64_t tokens, int64_t batch, int64_t groups, int64_t heads, int64_t kv_heads,
                                    int64_t head_dim, int64_t max_prefix, int64_t max_own) {
   MxPrefixPlan p;
+  const int64_t listed = groups;
   groups = mx_least(groups, tokens);
   p.prefix = mx_attention_plan(tokens, groups, heads, kv_heads, head_dim, max_prefix, 0, 0);
   const int64_t rows = tokens * (heads / kv_heads);
@@ -179,12 +185,12 @@ inline MxPrefixPlan mx_prefix_plan(int64_t tokens, int64_t batch, int64_t groups
   }
   p.prefix.splits = (int)mx_least(s < 1 ? 1 : s, kMxMostSplits / 2);
   p.prefix.mixed = p.own.mixed = 0;
+  // Groups and sequences without rows have tile numbers too. Many of them (10,000 groups of which one has rows) times the
+  // pieces would be a launch of workgroups that only end, or none at all beyond 2^24.
+  const int64_t numbers = mx_part_tiles(rows, listed, p.prefix.few ? 16 : 128) * p.prefix.splits +
+                          mx_part_tiles(rows, batch, p.own.few ? 16 : 128) * p.own.splits;
+  if (!p.through && numbers * kv_heads > 1 << 15) p.prefix.splits = p.own.splits = 1;
   return p;
-}
-
-// row tiles of a launch, by their numbering (mx_rows)
-inline int64_t mx_part_tiles(int64_t packed, int64_t sequences, int rows) {
-  return (packed + rows - 1) / rows + sequences - 1;
 }
 
 inline int64_t mx_prefix_bytes(const MxPrefixPlan& p, int64_t tokens, int64_t heads, int64_t head_dim) {

@@ -137,6 +137,16 @@ def test_no_groups(gpu):
     assert torch.equal(got, nv.mxfp4_attention(c.q, c.cache, c.table, c.seq, c.cu))
 
 
+@pytest.mark.parametrize("before,behind", [(40000, 0), (0, 40000), (300, 300)])
+def test_many_groups_without_sequences(gpu, before, behind):
+    import torch
+    c = Shared(gpu, [(1, 3000 + i) for i in range(3)], [2900], [0, 3], dim=128, page=64, group=4, kv_heads=2)
+    c.prefix_table = torch.nn.functional.pad(c.prefix_table, (0, 0, before, behind), value=-1)
+    c.prefix_lens = torch.nn.functional.pad(c.prefix_lens, (before, behind), value=64)
+    c.group_starts = torch.nn.functional.pad(torch.nn.functional.pad(c.group_starts, (before, 0)), (0, behind), value=3)
+    c.check_shared(c.run())
+
+
 @pytest.mark.parametrize("dim,heads,per,q,prefix,own", [(128, 28, 24, 1, 20000, 900), (64, 16, 9, 3, 7001, 300), (128, 16, 6, 200, 2500, 400),
                                                         (256, 8, 16, 1, 3001, 200)])
 def test_long(gpu, dim, heads, per, q, prefix, own):

@@ -99,8 +99,8 @@ def prefix(kw):
     (dict(x_pages=-1), 1), (dict(x_groups=1 << 24), 2), (dict(x_pages=1 << 26, x_stride=1 << 26), 2), (dict(mp=0), 1), (dict(mo=0), 1),
     (dict(heads=3), 1), (dict(heads=0), 1), (dict(scale=0.0), 1), (dict(scale=float("inf")), 1), (dict(scale=2.0 ** 127), 0),
     (dict(q=None), 1), (dict(out=None), 1), (dict(qh=60), 3), (dict(ot=64), 1), (dict(ws=None), 4), (dict(wb=64), 4), (dict(ws=FAKE + 4), 3),
-    (dict(b_tokens=(1 << 24) - 1), 0), (dict(b_tokens=1 << 24), 2), (dict(x_groups=(1 << 23) - 2, x_stride=2), 0),
-    (dict(x_groups=1 << 23, x_stride=2), 2), (dict(b_tokens=0, q=None, out=None, ws=None, wb=0, x_table=None), 0),
+    (dict(b_tokens=(1 << 24) - 1), 0), (dict(b_tokens=1 << 24), 2), (dict(x_groups=(1 << 23) - 5, x_stride=2), 0),
+    (dict(x_groups=(1 << 23) - 4, x_stride=2), 2), (dict(x_groups=1 << 22, b_batch=(1 << 22) - 3), 0), (dict(x_groups=1 << 22, b_batch=(1 << 22) - 2), 2), (dict(b_tokens=0, q=None, out=None, ws=None, wb=0, x_table=None), 0),
 ])
 def test_attention_prefix(kw, status):
     want = passed(status)
@@ -118,6 +118,8 @@ def test_prefix_workspace():
     assert prefix({})[1] == 2 * 8 * 4 * 66 * 4 + 8 * 4
     assert prefix(dict(b_tokens=0))[1] == 0
     assert prefix(dict(mp=1 << 17))[1] > prefix({})[1]
+    # groups without rows take a share of the launch: with very many of them there are no further pieces
+    assert prefix(dict(mp=1 << 17, x_groups=1 << 16))[1] == prefix({})[1]
     c, b = structs({})
     x = mxfp4._CPrefix(None, None, None, 0, 0, 0)
     assert nv.lib().mxfp4_attention_prefix_workspace_bytes(c, b, x, 4, 1, 1 << 17) == \
