@@ -89,7 +89,7 @@ def mxfp4_pages_fork(pages: Mxfp4Pages, parents, children, stream=None, strict: 
     p, pt = _pages(pages)
     n = _lists(parents, "parents", children, "children")
     with _On(stream, *pt, parents, children) as on:
-        done = torch.empty((n,), dtype=torch.int32, device=on.device)
+        done = parents.new_empty((n,))
         if not nv._call("mxfp4_pages_fork", p, parents.data_ptr(), children.data_ptr(), n, done.data_ptr(), on.handle,
                         strict=strict):
             return None
@@ -116,7 +116,7 @@ def mxfp4_pages_reserve(pages: Mxfp4Pages, slots, lens, workspace=None, stream=N
     p, pt = _pages(pages)
     n = _lists(slots, "slots", lens, "lens")
     with _On(stream, *pt, slots, lens) as on:
-        done, src, dst = torch.empty((3, n), dtype=torch.int32, device=on.device).unbind()
+        done, src, dst = slots.new_empty((3, n)).unbind()
         workspace = _workspace(on, workspace, nv.lib().mxfp4_pages_reserve_workspace_bytes(p, n) if workspace is None else 0)
         if not nv._call("mxfp4_pages_reserve", p, slots.data_ptr(), lens.data_ptr(), n, done.data_ptr(), src.data_ptr(),
                         dst.data_ptr(), workspace.data_ptr(), workspace.numel(), on.handle, strict=strict):
@@ -136,24 +136,25 @@ def mxfp4_pages_compact(pages: Mxfp4Pages, out: Optional[Mxfp4Pages] = None, wor
     mxfp4_cache_copy (int32 [num_pages // 2], -1 behind the last), and how many pages are in use (int32 [1])."""
     p, pt = _pages(pages)
     with _On(stream, *pt) as on:
-        made = out is None
-        if made:
-            out = Mxfp4Pages(torch.empty(pages.block_table.shape, dtype=torch.int32, device=on.device), pages.seq_lens,
-                             torch.empty_like(pages.refs), pages.page_size)
-        o, ot = _pages(out)
-        if (o.slots, o.max_pages, o.num_pages, o.page_size) != (p.slots, p.max_pages, p.num_pages, p.page_size):
-            raise ValueError("out must be of the size of pages")
-        if any(t.device != on.device for t in ot):
-            raise ValueError("out must be on the device of pages")
-        if not made:
+        if out is None:
+            out = Mxfp4Pages(pages.block_table.new_empty((p.slots, p.max_pages)), pages.seq_lens, torch.empty_like(pages.refs),
+                             pages.page_size)
+            table, stride, refs, lens = out.block_table.data_ptr(), p.max_pages, out.refs.data_ptr(), p.seq_lens
+        else:
+            o, ot = _pages(out)
+            if (o.slots, o.max_pages, o.num_pages, o.page_size) != (p.slots, p.max_pages, p.num_pages, p.page_size):
+                raise ValueError("out must be of the size of pages")
+            if any(t.device != on.device for t in ot):
+                raise ValueError("out must be on the device of pages")
             on.use(*ot)
-        moves = torch.empty((2 * (p.num_pages // 2) + 1,), dtype=torch.int32, device=on.device)
-        src, dst, used = moves.split((p.num_pages // 2, p.num_pages // 2, 1))
+            table, stride, refs, lens = o.block_table, o.table_stride, o.refs, o.seq_lens
+        moves = p.num_pages // 2
+        src, dst, used = pages.refs.new_empty((2 * moves + 1,)).split((moves, moves, 1))
         workspace = _workspace(on, workspace, nv.lib().mxfp4_pages_compact_workspace_bytes(p) if workspace is None else 0)
-        if not nv._call("mxfp4_pages_compact", p, o.block_table, o.table_stride, o.refs, src.data_ptr(), dst.data_ptr(),
-                        used.data_ptr(), workspace.data_ptr(), workspace.numel(), on.handle, strict=strict):
+        if not nv._call("mxfp4_pages_compact", p, table, stride, refs, src.data_ptr(), dst.data_ptr(), used.data_ptr(),
+                        workspace.data_ptr(), workspace.numel(), on.handle, strict=strict):
             return None
-        if o.seq_lens != p.seq_lens:
+        if lens != p.seq_lens:
             out.seq_lens.copy_(pages.seq_lens)
     return out, src, dst, used
 

@@ -13,7 +13,7 @@ import torch
 
 import nvfp4_block_scaled_swiglu_amd as nv
 
-from .mxfp4 import (Mxfp4Cache, _batch, _bf16, _cache, _CNorm, _CRotation, _On, _strides)
+from .mxfp4 import (Mxfp4Cache, _batch, _bf16, _cache, _CNorm, _CRotation, _On, _strides, _Tensor)
 
 
 @dataclass
@@ -44,7 +44,7 @@ def mxfp4_rotation(rotary_dim: int, device, theta: float = 10000.0, sections: Op
 
 
 def _vector(t, name: str, dtype, size: Optional[int] = None):
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != 1 or not t.is_cuda or not t.is_contiguous():
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.dim() != 1 or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous 1-D {str(dtype).split('.')[-1]} CUDA tensor")
     if size is not None and t.shape[0] != size:
         raise ValueError(f"{name} must have {size} elements, not {t.shape[0]}")
@@ -105,7 +105,7 @@ def mxfp4_norm_rope(x, rotation: Optional[Mxfp4Rotation] = None, positions=None,
     n, nt = _norm(weight, eps, "weight", dim)
     with _On(stream, x, *rt, *nt) as on:
         if out is None:
-            out = torch.empty((tokens, heads, dim), dtype=torch.bfloat16, device=on.device)
+            out = x.new_empty((tokens, heads, dim))
         elif _bf16(out, "out", 3, x.shape).device != on.device:
             raise ValueError("out must be on the device of x")
         else:
@@ -138,7 +138,7 @@ def mxfp4_norm_rope_append(cache: Mxfp4Cache, q, k, v, block_table, seq_lens, cu
     kn, kt = _norm(k_weight, eps, "k_weight", dim)
     with _On(stream, q, k, v, *ct, *bt, *rt, *qt, *kt) as on:
         if out is None:
-            out = torch.empty((tokens, heads, dim), dtype=torch.bfloat16, device=on.device)
+            out = q.new_empty((tokens, heads, dim))
         elif _bf16(out, "out", 3, q.shape).device != on.device:
             raise ValueError("out must be on the device of q")
         else:
