@@ -137,6 +137,15 @@ def test_no_groups(gpu):
     assert torch.equal(got, nv.mxfp4_attention(c.q, c.cache, c.table, c.seq, c.cu))
 
 
+@pytest.mark.parametrize("count,groups,q", [(63, 1, 1), (64, 1, 1), (70, 3, 2), (63, 63, 1), (64, 62, 3), (66, 64, 1), (130, 65, 1)])
+def test_counts_around_a_wave(gpu, count, groups, q):
+    """Sequences and groups are looked up 64 at a time, up to 63 of both at once."""
+    starts = [g * count // groups for g in range(groups)] + [count - (groups == 62)]  # (of 62 the last sequence is in none)
+    lens = [(1 + i % q, 130 + i % 9 + 64 * (i % 3)) for i in range(count)]
+    c = Shared(gpu, lens, [128 - 64 * (g % 2) for g in range(groups)], starts, torn=True, dim=64, page=32, group=2)
+    c.check_shared(c.run())
+
+
 @pytest.mark.parametrize("before,behind", [(40000, 0), (0, 40000), (300, 300)])
 def test_many_groups_without_sequences(gpu, before, behind):
     import torch
