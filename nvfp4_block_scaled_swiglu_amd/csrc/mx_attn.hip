@@ -26,7 +26,7 @@ __device__ __forceinline__ bool pair_of(const MxAttnArgs& a, int64_t pair, int64
     head = (place - seq * a.c.kv_heads) * a.group + n % a.group;
     return true;
   }
-  token = pair / a.heads;
+  token = pair < (int64_t)1 << 32 ? (uint32_t)pair / (uint32_t)a.heads : pair / a.heads;
   head = (int)(pair - token * a.heads);
   return token >= mx_row_start(a.b, 0) && token < mx_row_start(a.b, a.b.batch);  // of no sequence: stays as it was
 }
@@ -41,11 +41,23 @@ __global__ __launch_bounds__(256) void mx_attention_join_few_kernel(MxAttnArgs a
   constexpr int L = D / 4, P = 64 / L;
   const int lane = threadIdx.x & 63;
   const int64_t pair = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int64_t token;
-  int head;
-  if (pair >= pairs || !pair_of(a, pair, token, head)) return;
+  if (pair >= pairs) return;
+  // The pieces are read before anything is known of them (otherwise after the row's sequence, the sums and the weights:
+  // 2,688 pairs of 11 pieces 5.9 -> 5.4 us, with the launch before it 36.6 -> 34.8), also for pairs that turn out to be none and past the last piece, where
+  // the first is read again; what a piece that saw nothing left there is not used.
   float2 v = make_float2(-INFINITY, 0.0f);
   if (lane < a.splits) v = a.part_ml[lane * pairs + pair];
+  constexpr int kFirst = J / P < 8 ? J / P : 8;  // splits of a lane that are read so
+  f32x4_t o[kFirst];
+  const float* src = a.part_o + pair * D + (lane % L) * 4;
+#pragma unroll
+  for (int q = 0; q < kFirst; ++q) {
+    const int s = lane / L + q * P;
+    o[q] = *(const f32x4_t*)(src + (s < a.splits ? s : 0) * pairs * D);
+  }
+  int64_t token;
+  int head;
+  if (!pair_of(a, pair, token, head)) return;
   if (lane < a.prefix_splits && !a.shared[token]) v.y = 0.0f;
   if (v.y == 0.0f) v.x = -INFINITY;  // saw nothing; its o was not written
   float top = v.x;
@@ -58,22 +70,26 @@ __global__ __launch_bounds__(256) void mx_attention_join_few_kernel(MxAttnArgs a
   for (int off = J / 2; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
   sum = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(sum)));
   const float weight = v.y == 0.0f ? -1.0f : f;
-  // what a split that saw nothing left there is read and not used
   f32x4_t y = {0.0f, 0.0f, 0.0f, 0.0f};
-  const float* src = a.part_o + pair * D + (lane % L) * 4;
-  for (int s0 = lane / L; s0 < J; s0 += 4 * P) {
-    if (s0 - lane / L >= a.splits) break;  // uniform
-    f32x4_t o[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int s = s0 + q * P;
-      o[q] = *(const f32x4_t*)(src + (s < a.splits ? s : 0) * pairs * D);
-    }
+  for (int q = 0; q < kFirst; ++q) {
+    const float w = __shfl(weight, lane / L + q * P, 64);  // -1 past the last
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float w = __shfl(weight, s0 + q * P, 64);  // -1 past the last
+    for (int i = 0; i < 4; ++i) y[i] += w == -1.0f ? 0.0f : w * o[q][i];
+  }
+  if constexpr (kFirst * P < J) {
+    for (int s0 = lane / L + kFirst * P; s0 - lane / L < a.splits; s0 += 4 * P) {  // uniform
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] += w == -1.0f ? 0.0f : w * o[q][i];
+      for (int q = 0; q < 4; ++q) {
+        const int s = s0 + q * P;
+        o[q] = *(const f32x4_t*)(src + (s < a.splits ? s : 0) * pairs * D);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float w = __shfl(weight, s0 + q * P, 64);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] += w == -1.0f ? 0.0f : w * o[q][i];
+      }
     }
   }
 #pragma unroll
@@ -95,11 +111,19 @@ __global__ __launch_bounds__(256) void mx_attention_join_kernel(MxAttnArgs a) {
   __shared__ f32x4_t part[256];
   const int tid = threadIdx.x;
   const int64_t pair = blockIdx.x, pairs = gridDim.x;
+  float2 v = make_float2(-INFINITY, 0.0f);
+  if (tid < a.splits) v = a.part_ml[tid * pairs + pair];
+  constexpr int kFirst = 8;  // splits of a thread that are read ahead
+  f32x4_t o[kFirst];
+  const float* src = a.part_o + pair * D + (tid % L) * 4;
+#pragma unroll
+  for (int q = 0; q < kFirst; ++q) {
+    const int s = tid / L + q * P;
+    o[q] = *(const f32x4_t*)(src + (s < a.splits ? s : 0) * pairs * D);
+  }
   int64_t token;
   int head;
   if (!pair_of(a, pair, token, head)) return;
-  float2 v = make_float2(-INFINITY, 0.0f);
-  if (tid < a.splits) v = a.part_ml[tid * pairs + pair];
   if (tid < a.prefix_splits && !a.shared[token]) v.y = 0.0f;
   if (v.y == 0.0f) v.x = -INFINITY;  // saw nothing; its o was not written
   auto all = [&](float x, bool max) __attribute__((always_inline)) {
@@ -118,11 +142,16 @@ __global__ __launch_bounds__(256) void mx_attention_join_kernel(MxAttnArgs a) {
   const float sum = all(v.y == 0.0f ? 0.0f : f * v.y, false);
   if (tid < a.splits) weight[tid] = v.y == 0.0f ? -1.0f : f;
   __syncthreads();
-  // what a split that saw nothing left there is read and not used
   f32x4_t y = {0.0f, 0.0f, 0.0f, 0.0f};
-  const float* src = a.part_o + pair * D + (tid % L) * 4;
+#pragma unroll
+  for (int q = 0; q < kFirst; ++q) {
+    const int s = tid / L + q * P;
+    const float w = s < a.splits ? weight[s] : -1.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] += w == -1.0f ? 0.0f : w * o[q][i];
+  }
 #pragma unroll 8
-  for (int s = tid / L; s < a.splits; s += P) {
+  for (int s = tid / L + kFirst * P; s < a.splits; s += P) {
     const float w = weight[s];
     const f32x4_t o = *(const f32x4_t*)(src + s * pairs * D);
 #pragma unroll
