@@ -264,8 +264,8 @@ typedef struct {
  *                  multiples of 8, at most 2^31); 16-byte aligned. out_dev may be x_dev with the
  *                  same strides. head_dim 64, 128 or 256; heads 1 to 65536; tokens < 2^26.
  * norm, rotation : each may be NULL (left out).
- * Sums and products are fp32 (fp64 for heads whose squares leave its range). A head with an
- * infinity or a NaN comes out as the formulas have it.
+ * Sums and products are fp32 (fp64 for heads whose squares leave its range, and with an eps above 2^100).
+ * A head with an infinity or a NaN comes out as the formulas have it.
  */
 int mxfp4_norm_rope(const void* x_dev, int64_t x_token_stride, int64_t x_head_stride, int64_t tokens, int64_t heads,
                     int64_t head_dim, const mxfp4_norm* norm, const mxfp4_rotation* rotation, void* out_dev,

@@ -215,7 +215,8 @@ __global__ __launch_bounds__(64 * kWaves) void mx_rope_kernel(MxRopeArgs a) {
         Sixteen w;
         if (a.q_norm.weight) w = load(a.q_norm.weight, first, second);
         else w.w[0] = w.w[1] = u32x4_t{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-        if (__any(!(sum > 0x1p-80f && sum < 0x1p100f))) {  // squares may have left fp32's range
+        // squares may have left fp32's range, or eps does (one too small for it is nothing beside such sums)
+        if (__any(!(sum > 0x1p-80f && sum < 0x1p100f) || a.q_norm.eps > 0x1p100)) {
           double d = 0.0;
 #pragma unroll
           for (int i = 0; i < 16; ++i) d = fma((double)y[i], (double)y[i], d);
