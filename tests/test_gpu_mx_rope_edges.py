@@ -47,3 +47,26 @@ def test_queries_and_keys_of_an_append(gpu, eps):
     k = nv.mxfp4_cache_read(c.cache, c.table, c.seq, c.cu, 9)[0].double().cpu().numpy()
     want = ref.norm_rope(mx_ref.bits_to_f64(bits), eps=eps)[0]
     np.testing.assert_array_equal(k, mx_ref.round_trip(mx_ref.f64_to_bits(want)))
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_a_head_does_not_depend_on_those_beside_it(gpu, dim):
+    """Bit for bit: heads split differently over ranks come out the same, whatever else is in the row
+    (zeros, numbers whose squares leave fp32, infinities, NaN)."""
+    import torch
+    import nvfp4_block_scaled_swiglu_amd as nv
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    tokens, heads = 400, 2 * 1024 // dim + 3
+    x = torch.randn(tokens, heads, dim, generator=g, device=gpu).bfloat16()
+    w = (1 + 0.2 * torch.randn(dim, generator=g, device=gpu)).bfloat16()
+    rot = nv.mxfp4_rotation(dim, gpu)
+    pos = torch.arange(tokens, dtype=torch.int32, device=gpu)
+    want = nv.mxfp4_norm_rope(x, rot, pos, weight=w, eps=1e-6)
+    for other in (0.0, 2.0 ** 120, 2.0 ** -100, float("inf"), float("nan")):
+        y = x.clone()
+        y[:, 1::2] = other
+        got = nv.mxfp4_norm_rope(y, rot, pos, weight=w, eps=1e-6)
+        assert torch.equal(got[:, ::2], want[:, ::2]), other
+    for h in (0, 1, heads - 1):
+        alone = nv.mxfp4_norm_rope(x[:, h:h + 1], rot, pos, weight=w, eps=1e-6)
+        assert torch.equal(alone, want[:, h:h + 1]), h
