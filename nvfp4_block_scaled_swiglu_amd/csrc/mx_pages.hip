@@ -27,6 +27,12 @@ __device__ __forceinline__ int pages_of(const MxPages& p, int len) {
   return n < p.max_pages ? n : p.max_pages;
 }
 
+// the tokens of a slot, which its row has room for (below 2^30)
+__device__ __forceinline__ int length_of(const MxPages& p, int slot) {
+  const int len = p.lens[slot], most = p.max_pages << p.page_shift;
+  return len < 0 ? 0 : len < most ? len : most;
+}
+
 __device__ __forceinline__ bool is_page(const MxPages& p, int page) { return page >= 0 && page < p.num_pages; }
 
 constexpr int kTogether = 8;  // list entries of a workgroup
@@ -79,7 +85,7 @@ __global__ __launch_bounds__(1024) void mx_pages_free_kernel(MxPages p, const in
   __syncthreads();
   if (threadIdx.x < kTogether) {
     const int mine = at.slot[threadIdx.x], left = at.other[threadIdx.x];
-    const int len = mine >= 0 ? p.lens[mine] : 0;
+    const int len = mine >= 0 ? length_of(p, mine) : 0;
     at.begin[threadIdx.x] = pages_of(p, left);
     at.end[threadIdx.x] = left < len ? pages_of(p, len) : 0;
     if (left < len) p.lens[mine] = left;
@@ -130,9 +136,9 @@ __global__ __launch_bounds__(1024) void mx_pages_fork_kernel(MxPages p, const in
   __syncthreads();
   if (threadIdx.x < kTogether) {
     const int i = first + threadIdx.x, no = bad[threadIdx.x];
-    const int len = no ? 0 : p.lens[at.other[threadIdx.x]];
+    const int len = no ? 0 : length_of(p, at.other[threadIdx.x]);
     at.end[threadIdx.x] = pages_of(p, len);
-    if (!no) p.lens[at.slot[threadIdx.x]] = len > 0 ? len : 0;
+    if (!no) p.lens[at.slot[threadIdx.x]] = len;
     if (i < n) done[i] = !no;
   }
   __syncthreads();
@@ -297,7 +303,7 @@ __global__ __launch_bounds__(kPlan) void mx_pages_plan_kernel(MxPages p, const i
       to = lens[i];
       if (slot >= 0 && slot < p.slots) {
         const int first = __hip_atomic_load(work.mark + slot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        len = p.lens[slot] > 0 ? p.lens[slot] : 0;
+        len = length_of(p, slot);
         const int have = pages_of(p, len);
         if (first == i && to >= len && (int64_t)to <= (int64_t)p.max_pages << p.page_shift) {
           if (to > len && (len & ((1 << p.page_shift) - 1)) != 0) {
@@ -367,7 +373,7 @@ __global__ __launch_bounds__(kThreads) void mx_pages_enter_kernel(MxPages p, con
   if (i >= n) return;
   const int slot = slots[i];
   const int2 plan = work.plan[i];
-  const int len = plan.y >= 0 && p.lens[slot] > 0 ? p.lens[slot] : 0;
+  const int len = plan.y >= 0 ? length_of(p, slot) : 0;
   enter(p, i, plan, *work.found, slot, lens[i], len, done, src, dst, work.fresh);
 }
 
