@@ -14,7 +14,7 @@ import torch
 
 import nvfp4_block_scaled_swiglu_amd as nv
 
-from .mxfp4 import Mxfp4Cache, _buffer, _cache, _CPages, _int32, _On
+from .mxfp4 import Mxfp4Cache, _buffer, _cache, _CPages, _int32, _MOST, _On
 
 
 @dataclass
@@ -48,6 +48,8 @@ def _pages(p: Mxfp4Pages):
     slots, pages = p.block_table.shape
     if p.seq_lens.shape[0] != slots:
         raise ValueError("pages.block_table and pages.seq_lens disagree about the slots")
+    if not -_MOST <= p.page_size <= _MOST:
+        raise ValueError("pages.page_size must fit 64 bits")
     stride = p.block_table.stride(0) if slots > 1 else pages
     return (_CPages(p.block_table.data_ptr(), p.seq_lens.data_ptr(), p.refs.data_ptr(), slots, pages, stride, p.refs.shape[0],
                     p.page_size), (p.block_table, p.seq_lens, p.refs))

@@ -76,3 +76,17 @@ def test_lengths_are_clamped_in_long_lists(gpu):
     assert bool((done == 1).all()) and bool((src == -1).all()) and bool((dst == -1).all())
     assert torch.equal(p.seq_lens.clamp(0, 48), want) and bool((p.refs == 1).all())
     assert nv.mxfp4_pages_reserve(p, every, torch.full_like(every, 47))[0].tolist() == (every % 4 == 1).int().tolist()
+
+
+@pytest.mark.parametrize("size", [2 ** 64 + 16, 2 ** 63, -2 ** 64 + 16, -2 ** 63 - 1])
+def test_page_size_beyond_64_bits(gpu, size):
+    """Refused, not cut to 64 bits on its way into the library."""
+    nv, p, ints = begun(gpu)
+    p.page_size = size
+    before = [t.clone() for t in (p.block_table, p.seq_lens, p.refs)]
+    for call in (lambda: nv.mxfp4_pages_free(p, ints([0])), lambda: nv.mxfp4_pages_fork(p, ints([0]), ints([2])),
+                 lambda: nv.mxfp4_pages_reserve(p, ints([0]), ints([48])), lambda: nv.mxfp4_pages_compact(p),
+                 lambda: nv.mxfp4_pages_reserve_workspace_bytes(p, 1), lambda: nv.mxfp4_pages_compact_workspace_bytes(p)):
+        with pytest.raises(ValueError):
+            call()
+    assert all(bool((a == b).all()) for a, b in zip(before, (p.block_table, p.seq_lens, p.refs)))
