@@ -220,8 +220,8 @@ int64_t mxfp4_attention_prefix_workspace_bytes(const mxfp4_cache* cache, const m
  * own tokens is its own.
  * max_prefix, max_own : the longest prefix, and the most tokens of a sequence behind its own, as
  *                       far as the caller knows (> 0). They only decide how the work is split.
- * The rest as in mxfp4_attention; tokens * heads < 2^26 and (tokens * heads / kv_heads / 16 * 2 + batch +
- * groups) * kv_heads < 2^24.
+ * The rest as in mxfp4_attention; tokens * heads at most 2^26 - 4 and (tokens * heads / kv_heads / 16 * 2 +
+ * batch + groups) * kv_heads < 2^24.
  */
 int mxfp4_attention_prefix(const mxfp4_cache* cache, const mxfp4_batch* batch, const mxfp4_prefix* prefix,
                            const void* q_dev, int64_t q_token_stride, int64_t q_head_stride, int64_t heads, float scale,

@@ -267,7 +267,8 @@ int check_prefix(const mxfp4_cache* cache, const mxfp4_batch* batch, const mxfp4
   if (prefix->groups >= 1 << 24 || prefix->max_pages >= (int64_t)1 << 27 ||
       prefix->max_pages << b->page_shift >= (int64_t)1 << 30)
     return api_fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "prefixes beyond 2^24 groups or 2^30 tokens");
-  if (b->tokens * heads >= (int64_t)1 << 26 ||
+  // of the join, four rows x heads a workgroup, and of the parts, 16 packed rows each at least
+  if ((b->tokens * heads + 3) / 4 > kMostGroups ||
       (b->tokens * (heads / c->kv_heads) / 16 * 2 + b->batch + prefix->groups) * c->kv_heads > kMostGroups)
     return api_fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "too many rows and heads for one call");
   if (prefix->groups > 0 && b->batch > 0 && b->tokens > 0) {
