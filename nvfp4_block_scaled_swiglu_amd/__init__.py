@@ -22,6 +22,7 @@ Functions carry the C names:
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 import threading
 from dataclasses import dataclass
@@ -93,8 +94,14 @@ def lib() -> ctypes.CDLL:
             if not os.path.exists(LIB_PATH):
                 raise ImportError(f"{LIB_PATH} is missing: build it with "
                                   "`python nvfp4_block_scaled_swiglu_amd/build.py`")
+            # torch first where it is: it brings a HIP runtime of its own, and the library, which takes the
+            # one that is loaded, would otherwise come with another, for which there is then no device
+            try:
+                import torch  # noqa: F401
+            except ImportError:
+                pass
             l = ctypes.CDLL(LIB_PATH)
-            from .mxfp4 import SIGNATURES as mx_signatures
+            from .mxfp4_abi import SIGNATURES as mx_signatures
             for name, (res, args) in {**SIGNATURES, **mx_signatures}.items():
                 fn = getattr(l, name)
                 fn.restype = res
@@ -497,12 +504,33 @@ def nvfp4_silu_bf16(x, out=None, stream=None):
     return out
 
 
-from .mxfp4 import (  # noqa: E402  (the operators use the names above)
-    Mxfp4Cache, Mxfp4Tensor, empty_mxfp4, empty_mxfp4_cache, mxfp4_attention, mxfp4_attention_prefix,
-    mxfp4_attention_prefix_workspace_bytes, mxfp4_attention_workspace_bytes, mxfp4_cache_append, mxfp4_cache_read,
-    mxfp4_dequantize, mxfp4_gemm_bf16out, mxfp4_qdata_bytes, mxfp4_quantize, mxfp4_quantize_swiglu, mxfp4_scale_bytes,
-    mxfp4_scale_cols)
-from .mxfp4_pages import (  # noqa: E402
-    Mxfp4Pages, empty_mxfp4_pages, mxfp4_cache_copy, mxfp4_pages_compact, mxfp4_pages_compact_workspace_bytes,
-    mxfp4_pages_fork, mxfp4_pages_free, mxfp4_pages_reserve, mxfp4_pages_reserve_workspace_bytes)
-from .mxfp4_rope import Mxfp4Rotation, mxfp4_norm_rope, mxfp4_norm_rope_append, mxfp4_rotation  # noqa: E402
+# The MXFP4 operators, by the module that has them. Those modules import torch, which the package, its build and
+# the C functions do without, so each is imported with the first of its names.
+_OPERATORS = {name: module for module, names in {
+    "mxfp4_abi": ("mxfp4_qdata_bytes", "mxfp4_scale_bytes", "mxfp4_scale_cols"),
+    "mxfp4": ("Mxfp4Cache", "Mxfp4Tensor", "empty_mxfp4", "empty_mxfp4_cache", "mxfp4_attention",
+              "mxfp4_attention_prefix", "mxfp4_attention_prefix_workspace_bytes", "mxfp4_attention_workspace_bytes",
+              "mxfp4_cache_append", "mxfp4_cache_read", "mxfp4_dequantize", "mxfp4_gemm_bf16out", "mxfp4_quantize",
+              "mxfp4_quantize_swiglu"),
+    "mxfp4_pages": ("Mxfp4Pages", "empty_mxfp4_pages", "mxfp4_cache_copy", "mxfp4_pages_compact",
+                    "mxfp4_pages_compact_workspace_bytes", "mxfp4_pages_fork", "mxfp4_pages_free", "mxfp4_pages_reserve",
+                    "mxfp4_pages_reserve_workspace_bytes"),
+    "mxfp4_rope": ("Mxfp4Rotation", "mxfp4_norm_rope", "mxfp4_norm_rope_append", "mxfp4_rotation"),
+}.items() for name in names}
+_MODULES = ("mxfp4", "mxfp4_pages", "mxfp4_rope")
+
+
+def __getattr__(name: str):
+    if name in _MODULES:
+        return importlib.import_module("." + name, __name__)
+    if name not in _OPERATORS:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    value = globals()[name] = getattr(importlib.import_module("." + _OPERATORS[name], __name__), name)
+    return value
+
+
+def __dir__():
+    return sorted({*globals(), *_OPERATORS, *_MODULES})
+
+
+__all__ = [name for name in globals() if not name.startswith("_")] + list(_OPERATORS)
