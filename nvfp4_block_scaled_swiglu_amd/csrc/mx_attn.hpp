@@ -35,8 +35,8 @@ struct MxAttnArgs {
   float2* part_ml;  // [splits, tokens, heads] reference score and sum; by_seq likewise
   int skip;         // prompt form: sequences of up to so many packed rows are not its own
   bool by_seq;      // few-rows form: a workgroup a sequence and kv head, of up to 16 packed rows
-  int tiles;        // kMxPrefix and kMxOwn: row tiles of the launch
-  MxPrefix prefix;  // kMxPrefix and kMxOwn, whose launches always leave pieces
+  int tiles;        // all but kMxWhole: row tiles of the part
+  MxPrefix prefix;  // likewise (kMxPrefix and kMxOwn leave pieces always, kMxThrough where there are splits)
   int prefix_splits;        // joins: the first pieces are a prefix's, 0: none
   uint32_t* shared;         // [tokens] whether they hold for the row, written by kMxOwn for the join
 };
@@ -188,7 +188,7 @@ inline MxPrefixPlan mx_prefix_plan(int64_t tokens, int64_t batch, int64_t groups
   // Groups and sequences without rows have tile numbers too. Many of them (10,000 groups of which one has rows) times the
   // pieces would be a launch of workgroups that only end, or none at all beyond 2^24.
   const int64_t numbers = mx_part_tiles(rows, listed, p.prefix.few ? 16 : 128) * p.prefix.splits +
-                          mx_part_tiles(rows, batch, p.own.few ? 16 : 128) * p.own.splits;
+                          mx_part_tiles(rows, batch, 16) * p.own.splits;
   if (!p.through && numbers * kv_heads > 1 << 15) p.prefix.splits = p.own.splits = 1;
   return p;
 }
@@ -455,7 +455,7 @@ __device__ __forceinline__ MxSight mx_sight(const MxAttnArgs& a, const MxRows& r
                  a.window > 0 ? a.sinks : 0};
 }
 
-// Which piece, kv head and row tile a workgroup of a launch for a part has. Row tiles of a group read the
+// Which piece, kv head and row tile a workgroup of a part has. Row tiles of a group read the
 // same tokens, so where pieces and kv heads divide over the 8 XCDs (workgroup i is on XCD i % 8)
 // those of one piece and kv head follow one another on one XCD, whose L2 then has them.
 struct MxPlace {

@@ -74,6 +74,7 @@ constexpr int waves_per_simd(int d) { return d == 64 ? 3 : d == 128 ? 2 : 1; }  
 
 template <int D, MxPart PART>
 __device__ __forceinline__ void attend(const MxAttnArgs& a, const MxPlace& place) {
+  static_assert(PART != kMxOwn, "always the few-rows form's");
   using L = Lds<D>;
   constexpr int KS = D / 16, DB = D / 32;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -460,8 +461,7 @@ __device__ __forceinline__ void attend(const MxAttnArgs& a, const MxPlace& place
   if (!real) return;
   const int64_t token = rows.r0 + pn / g;
   const int head = kvh * g + pn % g;
-  if (PART == kMxPrefix || PART == kMxOwn || a.splits > 1) {
-    if (PART == kMxOwn && split == 0 && kvh == 0 && pn % g == 0 && h == 0) a.shared[token] = rows.shared;
+  if (PART == kMxPrefix || a.splits > 1) {
     const int64_t at = ((int64_t)split * a.b.tokens + token) * a.heads + head;
     if (h == 0) a.part_ml[at] = make_float2(*ref, all_sum);
     if (all_sum != 0.0f) {
