@@ -144,8 +144,22 @@ struct MxPrefixPlan {
 // each are best up to two: 4,512 in 240 48 us, 480 36; 3,500 in 384 29, 512 32. In the few-rows form up to 1,024 workgroups of 512
 // tokens at least: 64 packed rows of 12 groups over 8,200 tokens 31 us, in 2,048 workgroups 39. Of the rest: 1,024 tokens at
 // least, as its workgroups run beside the prefix's: 16 sequences over 6,000 of their own 44 us, 256 tokens
-// 57, 4,096 68. The rest is always the few-rows form's, which has no tiles of 128 to fill: 16 sequences of 35 packed
-// rows behind 8,200 48 us, in the prompt form 55; of 112 over 4,000 of their own 85 for 97.
+// 57, 4,096 68. (Between 12 and 29 tiles, between two and three workgroups of 64, and for heads of 256 nothing was measured.)
+//
+// The rest is always the few-rows form's, which has no tiles of 128 to fill. 32 heads of 128 over 8, us with the rest in
+// it, in the prompt form, and of mxfp4_attention, behind 8,000 shared tokens:
+//   packed rows   sequences   own tokens
+//    36            8            4,000        51   60   78
+//    36           64            8,000       349  567  624
+//   112            8              500        58   70  102
+//   112           24            4,000       211  185  251
+//   112           64            8,000       783  650 1102
+//   800            8            8,000       641  562  630
+//   800           24              500       759  710  824
+//   800           24            8,000      1852 1461 1537
+//   800           64            8,000      5022 3705 3931
+// So it gains up to two fifths with some 36 rows, and loses up to a third with 112 and more over long tokens of their
+// own, where the call can then take longer than mxfp4_attention, which shares nothing.
 constexpr int kMxJoinTokens = 800;
 
 inline int64_t mx_least(int64_t a, int64_t b) { return a < b ? a : b; }

@@ -12,7 +12,7 @@
 // What bounds it, 48 single tokens of 56 heads of 128 over 8 behind 8,200: the prefix's workgroups take 26 us (20 of them
 // 13 tiles, the rest their start and end), the sequences' own 10 us each in the CUs' other half, then 5 of joining: 35 us,
 // where mxfp4_attention reads the prefix 48 times in 80. 16 tokens of 32 heads of 128 over 4 behind 131,071: 45 us of
-// the prefix at 1.0 PFLOP/s, 8 of the rest behind it, 7.4 of joining 129 pieces: 56 to 62.
+// the prefix at 0.76 PFLOP/s, 8 of the rest behind it, 7.4 of joining 129 pieces: 56 to 62.
 #include "mx_attn_few.hpp"
 #include "mx_attn_prompt.hpp"
 

@@ -49,7 +49,8 @@ __device__ __forceinline__ void wave_sync() {
 
 // cosine and sine of position * freq. The product is exact as hi + lo (31 and 24 bits), and
 // so is its first product with 1 / 2 pi as a sum; whole turns are dropped before they cost
-// bits: 2^-52 of a turn at every position.
+// bits: 2^-52 of a turn at every position for frequencies up to 2^24, 2^-44 up to 2^32 (against exact rationals); from
+// there on a bit is lost with each of the frequency's, as 1 / 2 pi has 107 here.
 __device__ __forceinline__ double2 turn_of(int32_t position, float freq) {
   constexpr double kInv = 0.15915494309189535, kInvLo = -9.839338337591243e-18;  // 1 / 2 pi
   const double p = position, f = freq;

@@ -34,7 +34,13 @@ struct MxRopeArgs {
 // Waves of a token: one, which finds the angles once for all heads, where the tokens alone are two
 // waves for every SIMD; otherwise up to one for each step of the token's work (1024 / head_dim
 // heads of q, k or v), which wait side by side. 32,765 tokens of 32 and 8 heads of 128: 163 us with one, 185 with two,
-// 246 with six.
+// 246 with six. Of fewer tokens, into the cache, with one, two, four and all waves:
+//   256 tokens   32 and 8 heads of 128  9.1   7.2   6.4   5.5    56 and 8  12.1   8.2   6.6   6.6 (here 6.0)
+//   512                                 9.9   7.8   7.3   7.3              12.3   8.7   7.5   9.0
+//   1,024                              10.3   8.8   8.6  10.4              12.8  10.1   9.2  12.7
+//   2,048                              12.2  11.4  13.4  15.2              21.4  16.8  18.4  21.5
+//   4,096                              22.6  22.7  26.0  28.0              32.1  30.6  32.0  38.5
+// Heads of 64 and 256 go as 32 of 128 do; alone, without a cache, likewise.
 inline int64_t mx_rope_parts(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim) {
   const int64_t per = 1024 / head_dim;
   const int64_t steps = (heads + per - 1) / per + 2 * ((kv_heads + per - 1) / per);

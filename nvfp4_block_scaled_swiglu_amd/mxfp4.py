@@ -453,7 +453,7 @@ def mxfp4_attention_prefix(q, cache: Mxfp4Cache, block_table, seq_lens, cu_seqle
     prefix_table[g] (int32 [groups, max_pages]). Other tokens go by block_table, and so do all tokens of
     sequences in no group or whose first row does not see every shared token. max_prefix, max_own: the
     longest prefix, and the most tokens of a sequence behind its own, as far as known (by default
-    what the tables could hold); they decide how the work is split. workspace: a uint8 tensor of at least
+    what the tables could hold, which can take half as long again); they decide how the work is split. workspace: a uint8 tensor of at least
     mxfp4_attention_prefix_workspace_bytes(...) bytes, allocated by default."""
     c, ct = _cache(cache)
     _bf16(q, "q", 3)

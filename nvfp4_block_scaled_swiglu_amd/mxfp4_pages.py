@@ -111,7 +111,8 @@ def _bytes(size: int) -> int:
 
 def mxfp4_pages_reserve(pages: Mxfp4Pages, slots, lens, workspace=None, stream=None, strict: Optional[bool] = None):
     """Lengthen the sequences in `slots` to `lens` tokens (int32 [n] both), with new pages for them.
-    Returns (done, src, dst), int32 [n] each: done[i] is 1 where that was possible, and page src[i], of
+    Returns (done, src, dst), int32 [n] each: done[i] is 1 where that was possible (also behind entries that there
+    were too few pages for, if it needs none), and page src[i], of
     which others hold the beginning too, has to be copied to dst[i] in every cache
     (mxfp4_cache_copy; -1: nothing to copy) before the sequence's next token is written and before
     pages are given out again."""
