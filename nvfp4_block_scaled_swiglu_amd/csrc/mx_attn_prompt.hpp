@@ -318,10 +318,12 @@ __device__ __forceinline__ void attend(const MxAttnArgs& a, const MxPlace& place
   auto phase_scores = [&](f32x16_t& x, const f32x16_t& y, int vbuf, int half) __attribute__((always_inline)) {
     constexpr int G = 4;  // groups of weights, over KS steps; packed a step after they are taken
     float p[2][4];
-    // Before the SIMD's other waves: the exponentials are the longer chain. (8 sequences of 288 to 512 rows behind
-    // 6,144 tokens 635 -> 622 us; prompts of 4,096, 32 heads of 128 over 8, 157 -> 150, of 2,048, 56 heads, 81 -> 77. Not
-    // everywhere: of 2,048, 32 heads of 128 64 -> 66, of 64 43.5 -> 46.5.)
-    __builtin_amdgcn_s_setprio(1);
+    // Before the SIMD's other waves: the exponentials are the longer chain (8 sequences of 288 to 512 rows behind
+    // 6,144 tokens 635 -> 622 us). Not for whole calls, where it moves 120 kinds of prompts by 11 % either way: those of 64 are
+    // 0.9 % slower with it on average (3,000 tokens of 56 heads over 8 97 -> 109 us), of 256 0.4 %, of 128 0.25 % faster (4,096 of
+    // 32 heads 158 -> 149, but 3,000 109 -> 114, and 2 ragged ones of 56 heads 781 -> 795).
+    constexpr bool kAhead = PART != kMxWhole;
+    if constexpr (kAhead) __builtin_amdgcn_s_setprio(1);
     zero(x);
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
@@ -335,7 +337,7 @@ __device__ __forceinline__ void attend(const MxAttnArgs& a, const MxPlace& place
       fence();
     }
     add(G - 1, p[(G - 1) & 1]);
-    __builtin_amdgcn_s_setprio(0);
+    if constexpr (kAhead) __builtin_amdgcn_s_setprio(0);
   };
 
   // Marked blocks: a product of "is NaN" with "is seen" tells the rows that get one, for the
